@@ -148,8 +148,9 @@ def _prepare_sample(case, g):
     dev = "cuda"
     N, V, ld, mode = case["N"], case["V"], case["ld"], case["mode"]
     logits = torch.randn(N, ld, generator=g, device=dev) * case["spread"]
-    # a handful of likely tokens above the bulk
-    likely = torch.randint(0, V, (N, 24), generator=g, device=dev)
+    # a handful of likely tokens above the bulk, one in each 24th of the vocabulary (a token drawn twice would get
+    # whichever of its two values is written last)
+    likely = torch.arange(24, device=dev) * (V // 24) + torch.randint(0, V // 24, (N, 24), generator=g, device=dev)
     logits.scatter_(1, likely, 3.0 * case["spread"] + 3.0 * torch.rand(N, 24, generator=g, device=dev))
     if case["masked"]:
         out = torch.rand(N, ld, generator=g, device=dev) < case["masked"]
