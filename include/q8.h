@@ -86,7 +86,8 @@ const char *q8_last_cuda_error(void);
  * outputs are incomplete), 2 = waiting for in-flight copies at exit ran out,
  * 4 = q8_moe_gemv skipped an expert pick (out of range, or repeated within a
  * token), 8 = a kernel found its launch configuration differing from its
- * plan (it returned without computing). */
+ * plan (it returned without computing), 16 = an adapter index past the bank
+ * (q8_lora and q8_gemv_lora took the row as one without an adapter). */
 q8_status q8_read_device_error(uint32_t *detail);
 
 /* Library version as MAJOR*10000 + MINOR*100 + PATCH. */
@@ -198,6 +199,76 @@ static inline float q8_argmax_value(uint64_t key) {
 }
 
 /* ---------------------------------------------------------------------- */
+/* Sampler: one token per row of logits                                    */
+/* ---------------------------------------------------------------------- */
+
+/* For each row n < N of logits [N][ld] (fp32, the first V of each row; ld >= V
+ * serves a padded vocabulary): token[n] drawn with the row's temperature and
+ * filters from the uniform number u[n], and prob[n] the probability it was
+ * drawn with.  The sampling counterpart of q8_gemv_argmax, for the logits that
+ * q8_gemv, q8_gemv_split and the other products write.
+ * With m the row's largest logit and w_i = exp((l_i - m) / temperature), in the
+ * order of l descending (equal logits: lowest index first):
+ *   top_k: the first top_k stay (off when <= 0 or >= V);
+ *   top_p: of those, each stays while the w before it sum to less than top_p
+ *     times the sum over all of them (off when >= 1; <= 0 keeps the first);
+ *   min_p: those with w >= min_p stay (off when <= 0; above 1 counts as 1);
+ * the first always stays.  token is the smallest index i whose kept w_j, j <= i,
+ * sum to more than u times the kept total; prob = w_token / the kept total.
+ * temperature <= 0 (or NaN): the arg-max, lowest index first, prob 1.
+ * temperature, top_k, top_p, min_p, u: [N] device arrays; a NULL temperature
+ * is 1, a NULL filter is off.  prob may be NULL.
+ * Any logits are defined: NaN counts as -inf; a logit of -inf is never drawn;
+ * +inf logits share the draw between them; a row with nothing above -inf gives
+ * token -1, prob 0.  u is taken into [0, 1) (below 0 and NaN: 0; 1 and above:
+ * the last kept token).  The sums are exact in units of 2^-43 of the largest
+ * weight, each weight rounded once (weights below 2^-44 are never drawn), so a
+ * token does not depend on the order of any sum: the same from run to run.
+ * One launch, no workspace.  1 <= N <= 65536, V <= 524288. */
+q8_status q8_sample(const float *logits, const float *temperature, const int32_t *top_k, const float *top_p,
+                    const float *min_p, const float *u, int32_t *token, float *prob, int64_t N, int64_t V,
+                    int64_t ld, q8_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Low-rank adapters of many requests beside a shared projection           */
+/* ---------------------------------------------------------------------- */
+
+/* Element type of adapter matrices. */
+typedef enum q8_dtype { Q8_F32 = 0, Q8_F16 = 1, Q8_BF16 = 2 } q8_dtype;
+
+/* y[n] = residual[n] + scale[a] B_a (A_a x[n]),  a = adapter[n], for n < N: the
+ * adapters alone, to stand beside any of the library's products (y of another
+ * call may be the residual, in place).  Rows with a negative adapter have none
+ * (y = residual); an index >= n_adapters is taken the same way and sets bit 16
+ * of the device error word.
+ * A: [n_adapters][R][K], B: [n_adapters][M][R], both of type `dtype` (q8_dtype),
+ *   16-byte aligned.  rank: [n_adapters] int32, the adapter's own rank (0..R;
+ *   outside values are clamped): rows of A and columns of B from there on are
+ *   not used, whatever they hold; NULL: R for all.  scale: [n_adapters] fp32 or
+ *   NULL (1).  adapter: [N] int32.  residual: [N][M] fp32 or NULL (0); it may be
+ *   y itself, any other overlap is undefined.  x: [N][K] fp32; y: [N][M] fp32.
+ * fp32 sums in a fixed order: |y - exact| <= 2^-24 times (K/256 + 40) times
+ *   |scale| sum_j |B_mj| sum_k |A_jk x_k|, plus the roundings of the stored
+ *   value; bit-identical from run to run.  An adapter's matrices are read once
+ *   for every 4 of its tokens.  One launch.
+ * K a multiple of 32, R a multiple of 8 up to 128, N <= 16, M <= 2^25. */
+q8_status q8_lora(const float *x, const void *A, const void *B, const int32_t *rank, const float *scale,
+                  const int32_t *adapter, const float *residual, float *y, int64_t M, int64_t K, int64_t N,
+                  int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream);
+
+/* y = W x + (what q8_lora gives): the shared projection of a batch whose rows
+ * carry adapters of their own.  W: packed M x K.  Two launches: q8_lora's
+ * kernel, then q8_gemv's (q8_gemv_split's) with the add in its store, whose
+ * weights stream in while the adapters are computed.  The product's bound is
+ * q8_gemv's (q8_gemv_split's); the rest as q8_lora. */
+q8_status q8_gemv_lora(const void *W, const float *x, const void *A, const void *B, const int32_t *rank,
+                       const float *scale, const int32_t *adapter, const float *residual, float *y, int64_t M,
+                       int64_t K, int64_t N, int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream);
+q8_status q8_gemv_lora_split(const void *W, const float *x, const void *A, const void *B, const int32_t *rank,
+                             const float *scale, const int32_t *adapter, const float *residual, float *y, int64_t M,
+                             int64_t K, int64_t N, int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
 /* K-quant GEMV: Q4_K and Q6_K weights in their raw GGUF layout            */
 /* ---------------------------------------------------------------------- */
 
@@ -281,6 +352,31 @@ q8_status q8_gate_up_swiglu_split(const void *W, const float *x, float *h, int64
  * Limits: 1 <= T <= 16, 1 <= top_k <= min(E, 8), E <= 256. */
 q8_status q8_moe_route(const float *logits, int64_t T, int64_t E, int64_t top_k,
                        int renormalize, int32_t *idx, float *w, q8_stream_t stream);
+
+/* Score functions of q8_moe_route_grouped. */
+typedef enum q8_score { Q8_SCORE_SOFTMAX = 0, Q8_SCORE_SIGMOID = 1 } q8_score;
+
+/* q8_moe_route with biased and grouped selection.  For each token: scores s =
+ * softmax (over all E) or sigmoid of the logits; selection scores c = s + bias
+ * (bias NULL: c = s).  The experts form n_group groups of E / n_group
+ * consecutive ones; a group's score is the sum of its group_top (1 or 2)
+ * largest c, and the topk_group best groups stay (n_group = 1: all experts).
+ * idx[t]: the top_k experts of those by c, descending; equal scores, of groups
+ * and of experts, go to the lowest index.  w[t][j] = s[idx] (not c), divided
+ * by the picks' sum when renormalize != 0, times scale.
+ * Scores are held and compared in double, w is rounded once.  NaN logits count
+ * as -inf; a score of -inf logits is 0, and +inf logits share a softmax; a NaN
+ * selection score (of a NaN bias, or of groups holding both infinities) counts
+ * as -inf; w is 0 where the picks' sum is 0.  The picks are always top_k
+ * different experts of the groups that stay.
+ * logits: [T][E] fp32.  bias: [E] fp32 or NULL.  idx: [T][top_k] int32, w:
+ * [T][top_k] fp32, as q8_moe_gemv reads them (T there is at most 16: a longer
+ * list is routed at once and its tokens' blocks run 16 at a time).
+ * Limits: T <= 2^20, E <= 256, top_k <= 8, n_group <= 32 dividing E, group_top
+ * <= E / n_group when n_group > 1, top_k <= topk_group * E / n_group. */
+q8_status q8_moe_route_grouped(const float *logits, const float *bias, int64_t T, int64_t E, int64_t top_k,
+                               int64_t n_group, int64_t topk_group, int group_top, int score, int renormalize,
+                               float scale, int32_t *idx, float *w, q8_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* S6  Grouped MoE GEMV over the routed experts                            */

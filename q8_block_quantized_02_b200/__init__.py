@@ -27,7 +27,13 @@ __all__ = [
     "q8_moe_gemv_noalloc",
     "q8_quantize_act", "q8_rmsnorm_quantize_act", "q8q8_gemv", "q8q8_block_dots",
     "q8_test_wait_timeout", "q8_gemv_split", "q8_gate_up_swiglu_split",
+    "Q8_F32", "Q8_F16", "Q8_BF16", "q8_lora", "q8_gemv_lora", "q8_gemv_lora_split",
+    "Q8_SCORE_SOFTMAX", "Q8_SCORE_SIGMOID", "q8_moe_route_grouped", "q8_sample",
 ]
+
+# the header's q8_dtype and q8_score
+Q8_F32, Q8_F16, Q8_BF16 = 0, 1, 2
+Q8_SCORE_SOFTMAX, Q8_SCORE_SIGMOID = 0, 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _lock = threading.Lock()
@@ -71,6 +77,12 @@ _SIGS = {
     "q8_test_wait_timeout": (_INT, [ctypes.c_uint32, _P, _P]),
     "q8_gemv_split": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P]),
     "q8_gate_up_swiglu_split": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P]),
+    "q8_lora": (_INT, [_P] * 8 + [_I64] * 5 + [_INT, _P]),
+    "q8_gemv_lora": (_INT, [_P] * 9 + [_I64] * 5 + [_INT, _P]),
+    "q8_gemv_lora_split": (_INT, [_P] * 9 + [_I64] * 5 + [_INT, _P]),
+    "q8_moe_route_grouped": (_INT, [_P, _P, _I64, _I64, _I64, _I64, _I64, _INT, _INT, _INT, ctypes.c_float, _P, _P,
+                                    _P]),
+    "q8_sample": (_INT, [_P] * 8 + [_I64] * 3 + [_P]),
 }
 
 
@@ -282,3 +294,33 @@ def q8_gemv_split(W, x, y, M, K, N, stream=None):
 
 def q8_gate_up_swiglu_split(W, x, h, I, K, N, stream=None):
     _call("q8_gate_up_swiglu_split", _ptr(W), _ptr(x), _ptr(h), I, K, N, _stream(stream))
+
+
+def q8_lora(x, A, B, rank, scale, adapter, residual, y, M, K, N, n_adapters, R, dtype, stream=None):
+    """rank, scale and residual may be None; residual may be y itself.  dtype: Q8_F32, Q8_F16 or Q8_BF16."""
+    _call("q8_lora", _ptr(x), _ptr(A), _ptr(B), _ptr(rank), _ptr(scale), _ptr(adapter), _ptr(residual), _ptr(y), M, K,
+          N, n_adapters, R, int(dtype), _stream(stream))
+
+
+def q8_gemv_lora(W, x, A, B, rank, scale, adapter, residual, y, M, K, N, n_adapters, R, dtype, stream=None):
+    """As q8_lora, plus W x."""
+    _call("q8_gemv_lora", _ptr(W), _ptr(x), _ptr(A), _ptr(B), _ptr(rank), _ptr(scale), _ptr(adapter), _ptr(residual),
+          _ptr(y), M, K, N, n_adapters, R, int(dtype), _stream(stream))
+
+
+def q8_gemv_lora_split(W, x, A, B, rank, scale, adapter, residual, y, M, K, N, n_adapters, R, dtype, stream=None):
+    _call("q8_gemv_lora_split", _ptr(W), _ptr(x), _ptr(A), _ptr(B), _ptr(rank), _ptr(scale), _ptr(adapter),
+          _ptr(residual), _ptr(y), M, K, N, n_adapters, R, int(dtype), _stream(stream))
+
+
+def q8_moe_route_grouped(logits, bias, T, E, top_k, n_group, topk_group, group_top, score, renormalize, scale, idx, w,
+                         stream=None):
+    """bias may be None; score: Q8_SCORE_SOFTMAX or Q8_SCORE_SIGMOID."""
+    _call("q8_moe_route_grouped", _ptr(logits), _ptr(bias), T, E, top_k, n_group, topk_group, int(group_top),
+          int(score), int(renormalize), float(scale), _ptr(idx), _ptr(w), _stream(stream))
+
+
+def q8_sample(logits, temperature, top_k, top_p, min_p, u, token, prob, N, V, ld, stream=None):
+    """temperature, top_k, top_p, min_p and prob may be None."""
+    _call("q8_sample", _ptr(logits), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(token),
+          _ptr(prob), N, V, ld, _stream(stream))

@@ -17,6 +17,9 @@
 #include "resident.cuh"
 #include "moe.cuh"
 #include "kquant.cuh"
+#include "lora.cuh"
+#include "route_grouped.cuh"
+#include "sample.cuh"
 #include "selftest.cuh"
 
 namespace q8 {
@@ -910,6 +913,78 @@ static q8_status run_q6k_packed(const void *P, const float *x, float *y, int64_t
     return Q8_OK;
 }
 
+// ---------------------------------------------------------------------------
+// low-rank adapters, beside a projection or alone
+// ---------------------------------------------------------------------------
+using LoraKernel = void (*)(LoraArgs);
+
+static LoraKernel lora_kernel_for(int dtype) {
+    return dtype == Q8_F32 ? &lora_kernel<float> : dtype == Q8_F16 ? &lora_kernel<__half> : &lora_kernel<__nv_bfloat16>;
+}
+
+static cudaError_t setup_lora_kernels(int) {
+    for (int d = 0; d < 3; ++d) {
+        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(lora_kernel_for(d)),
+                                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+static RegisterSetup g_reg_lora(setup_lora_kernels);
+
+static q8_status check_aligned4(const void *p, bool nullable) {
+    if (!p && nullable) return Q8_OK;
+    Q8_CHECK(check_device_ptr(p, false));
+    return (reinterpret_cast<uintptr_t>(p) & 3u) ? Q8_ERR_ALIGN : Q8_OK;
+}
+
+static q8_status lora_check(const LoraArgs &a, int64_t N, int64_t n_adapters, int64_t R, int dtype) {
+    if (a.M <= 0 || a.K <= 0 || N <= 0 || n_adapters <= 0 || R <= 0 || a.K % 32 || R % 8) return Q8_ERR_SHAPE;
+    if (N > kLoraMaxN || R > kLoraMaxR || n_adapters > (int64_t)1 << 20 || a.M > (int64_t)1 << 25 ||
+        a.K > (int64_t)1 << 24)
+        return Q8_ERR_UNSUPPORTED;
+    if (dtype != Q8_F32 && dtype != Q8_F16 && dtype != Q8_BF16) return Q8_ERR_INVALID;
+    Q8_CHECK(check_device_ptr(a.x));
+    Q8_CHECK(check_device_ptr(a.A));
+    Q8_CHECK(check_device_ptr(a.B));
+    Q8_CHECK(check_device_ptr(a.y));
+    Q8_CHECK(check_aligned4(a.rank, true));
+    Q8_CHECK(check_aligned4(a.scale, true));
+    Q8_CHECK(check_aligned4(a.adapter, false));
+    return check_aligned4(a.res, true);
+}
+
+// A cluster per token: 16 CTAs for up to 8 tokens, 8 for more (the clusters
+// then fill the SMs once).
+static q8_status run_lora(const LoraArgs &a, int dtype, cudaStream_t stream) {
+    const DeviceInfo *dev = nullptr;
+    Q8_CHECK(device_info(&dev));
+    const int cl = a.N <= 8 ? 16 : 8;
+    return launch_pdl_cluster(lora_kernel_for(dtype), dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), 0, stream,
+                              "q8_lora launch", (unsigned)cl, a);
+}
+
+// The adapters write y = residual + their part; the projection's store then
+// adds its product to y in place.
+static q8_status run_gemv_lora(const void *W, const LoraArgs &a, int64_t N, int64_t n_adapters, int64_t R, int dtype,
+                               cudaStream_t stream, bool split) {
+    Q8_CHECK(lora_check(a, N, n_adapters, R, dtype));
+    Q8_CHECK(check_device_ptr(W));
+    Q8_CHECK(run_lora(a, dtype, stream));
+    return run_tile(W, a.x, nullptr, a.y, a.M, a.K, N, kModeF32, stream, nullptr, a.y, split);
+}
+
+// ---------------------------------------------------------------------------
+// sampler
+// ---------------------------------------------------------------------------
+static cudaError_t setup_sample_kernel(int max_smem) {
+    const void *k = reinterpret_cast<const void *>(&sample_kernel);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+}
+static RegisterSetup g_reg_sample(setup_sample_kernel);
+
 }  // namespace q8
 
 using namespace q8;
@@ -1177,6 +1252,102 @@ q8_status q8_moe_route(const float *logits, int64_t T, int64_t E, int64_t top_k,
     return launch_pdl(route_kernel, dim3((unsigned)ceil_div(T, warps)), dim3(32 * warps), 0,
                       (cudaStream_t)stream, "q8_moe_route launch", logits, (int)T, (int)E,
                       (int)top_k, renormalize, idx, w);
+}
+
+q8_status q8_moe_route_grouped(const float *logits, const float *bias, int64_t T, int64_t E, int64_t top_k,
+                               int64_t n_group, int64_t topk_group, int group_top, int score, int renormalize,
+                               float scale, int32_t *idx, float *w, q8_stream_t stream) {
+    if (T <= 0 || E <= 0 || top_k <= 0 || n_group <= 0 || topk_group <= 0) return Q8_ERR_SHAPE;
+    if (E % n_group || topk_group > n_group || top_k > topk_group * (E / n_group)) return Q8_ERR_SHAPE;
+    if (T > (int64_t)1 << 20 || E > kRouteMaxE || top_k > kRouteMaxK || n_group > kRouteMaxGroups)
+        return Q8_ERR_UNSUPPORTED;
+    if (group_top != 1 && group_top != 2) return Q8_ERR_INVALID;
+    if (n_group > 1 && group_top > E / n_group) return Q8_ERR_SHAPE;
+    if (score != Q8_SCORE_SOFTMAX && score != Q8_SCORE_SIGMOID) return Q8_ERR_INVALID;
+    if (renormalize != 0 && renormalize != 1) return Q8_ERR_INVALID;
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return Q8_ERR_INVALID;  // NaN or infinite
+    Q8_CHECK(check_aligned4(logits, false));
+    Q8_CHECK(check_aligned4(bias, true));
+    Q8_CHECK(check_aligned4(idx, false));
+    Q8_CHECK(check_aligned4(w, false));
+    RouteArgs a{};
+    a.logits = logits;
+    a.bias = bias;
+    a.idx = idx;
+    a.w = w;
+    a.T = (int)T;
+    a.E = (int)E;
+    a.top_k = (int)top_k;
+    a.groups = (int)n_group;
+    a.keep = (int)topk_group;
+    a.group_top = group_top;
+    a.sigmoid = score == Q8_SCORE_SIGMOID;
+    a.renormalize = renormalize;
+    a.scale = scale;
+    return launch_pdl(route_grouped_kernel, dim3((unsigned)ceil_div(T, kRouteGWarps)), dim3(32 * kRouteGWarps), 0,
+                      (cudaStream_t)stream, "q8_moe_route_grouped launch", a);
+}
+
+q8_status q8_lora(const float *x, const void *A, const void *B, const int32_t *rank, const float *scale,
+                  const int32_t *adapter, const float *residual, float *y, int64_t M, int64_t K, int64_t N,
+                  int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream) {
+    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R};
+    Q8_CHECK(lora_check(a, N, n_adapters, R, dtype));
+    return run_lora(a, dtype, (cudaStream_t)stream);
+}
+
+q8_status q8_gemv_lora(const void *W, const float *x, const void *A, const void *B, const int32_t *rank,
+                       const float *scale, const int32_t *adapter, const float *residual, float *y, int64_t M,
+                       int64_t K, int64_t N, int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream) {
+    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R};
+    return run_gemv_lora(W, a, N, n_adapters, R, dtype, (cudaStream_t)stream, false);
+}
+
+q8_status q8_gemv_lora_split(const void *W, const float *x, const void *A, const void *B, const int32_t *rank,
+                             const float *scale, const int32_t *adapter, const float *residual, float *y, int64_t M,
+                             int64_t K, int64_t N, int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream) {
+    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R};
+    return run_gemv_lora(W, a, N, n_adapters, R, dtype, (cudaStream_t)stream, true);
+}
+
+q8_status q8_sample(const float *logits, const float *temperature, const int32_t *top_k, const float *top_p,
+                    const float *min_p, const float *u, int32_t *token, float *prob, int64_t N, int64_t V,
+                    int64_t ld, q8_stream_t stream) {
+    if (N <= 0 || V <= 0 || ld < V) return Q8_ERR_SHAPE;
+    if (N > (int64_t)1 << 16 || V > (int64_t)kSampleMaxSlice * kSampleMaxCluster || ld > (int64_t)1 << 31)
+        return Q8_ERR_UNSUPPORTED;
+    Q8_CHECK(check_aligned4(logits, false));
+    Q8_CHECK(check_aligned4(temperature, true));
+    Q8_CHECK(check_aligned4(top_k, true));
+    Q8_CHECK(check_aligned4(top_p, true));
+    Q8_CHECK(check_aligned4(min_p, true));
+    Q8_CHECK(check_aligned4(u, false));
+    Q8_CHECK(check_aligned4(token, false));
+    Q8_CHECK(check_aligned4(prob, true));
+    const DeviceInfo *dev = nullptr;
+    Q8_CHECK(device_info(&dev));
+    // A cluster per row, as many CTAs as the row needs to fit in their shared
+    // memory; more while the rows leave SMs free and a CTA keeps 1024 logits.
+    int cl = 1;
+    while (cl < kSampleMaxCluster && (ceil_div(V, cl) > kSampleMaxSlice ||
+                                      (N * cl * 2 <= dev->sms && ceil_div(V, cl * 2) >= 1024)))
+        cl *= 2;
+    SampleArgs a{};
+    a.logits = logits;
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.u = u;
+    a.token = token;
+    a.prob = prob;
+    a.ld = ld;
+    a.V = (int)V;
+    a.slice = (int)round_up(ceil_div(V, cl), 4);
+    const size_t smem = sizeof(SampleShared) + (size_t)a.slice * 4;
+    if (smem > (size_t)dev->max_smem_optin) return Q8_ERR_UNSUPPORTED;
+    return launch_pdl_cluster(sample_kernel, dim3((unsigned)(N * cl)), dim3(kSampleThreads), smem,
+                              (cudaStream_t)stream, "q8_sample launch", (unsigned)cl, a);
 }
 
 size_t q8_moe_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I,

@@ -26,6 +26,7 @@ enum : unsigned int {
     kErrDrainTimeout = 1u << 1,  // waiting for in-flight copies at exit ran out
     kErrBadExpert = 1u << 2,     // an expert index outside [0, E) was seen
     kErrLaunchConfig = 1u << 3,  // shared memory, cluster or tensor memory differ from the plan
+    kErrBadAdapter = 1u << 4,    // an adapter index past the bank was seen
 };
 
 __device__ unsigned int g_q8_error;
