@@ -1344,7 +1344,7 @@ q8_status q8_sample(const float *logits, const float *temperature, const int32_t
     a.ld = ld;
     a.V = (int)V;
     a.slice = (int)round_up(ceil_div(V, cl), 4);
-    const size_t smem = sizeof(SampleShared) + (size_t)a.slice * 4;
+    const size_t smem = sample_smem_bytes(a.slice, cl);
     if (smem > (size_t)dev->max_smem_optin) return Q8_ERR_UNSUPPORTED;
     return launch_pdl_cluster(sample_kernel, dim3((unsigned)(N * cl)), dim3(kSampleThreads), smem,
                               (cudaStream_t)stream, "q8_sample launch", (unsigned)cl, a);
