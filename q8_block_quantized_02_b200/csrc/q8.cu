@@ -1344,7 +1344,10 @@ q8_status q8_sample(const float *logits, const float *temperature, const int32_t
     a.ld = ld;
     a.V = (int)V;
     a.slice = (int)round_up(ceil_div(V, cl), 4);
-    const size_t smem = sample_smem_bytes(a.slice, cl);
+    // two CTAs fit on an SM; when the rows do not need that, ask for more than
+    // half an SM's shared memory so that each CTA gets an SM of its own
+    size_t smem = sample_smem_bytes(a.slice, cl);
+    if (N * cl <= dev->sms) smem = std::max(smem, (size_t)dev->max_smem_optin / 2 + 1024);
     if (smem > (size_t)dev->max_smem_optin) return Q8_ERR_UNSUPPORTED;
     return launch_pdl_cluster(sample_kernel, dim3((unsigned)(N * cl)), dim3(kSampleThreads), smem,
                               (cudaStream_t)stream, "q8_sample launch", (unsigned)cl, a);

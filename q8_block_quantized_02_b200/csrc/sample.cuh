@@ -12,13 +12,22 @@
 // largest weight, and a smaller weight is never drawn.)
 //
 // A row belongs to one thread-block cluster whose CTAs hold it in shared
-// memory, so the logits are read once.  A filter's threshold comes from a
-// 2048-bin histogram of the row (counts for top-k, mass for top-p) that the
-// cluster adds up over distributed shared memory; the crossing bin's elements
-// -- or everything down to that bin, when that is a short list -- are then
-// copied to every CTA, which settles the threshold among them on its own.  So a
-// row takes two or three cluster barriers; only runs of ties longer than the
-// list take more rounds.
+// memory, so the logits are read once.
+//   top-k: the k-th largest of the threads' own maxima bounds the k-th largest
+//     element from below, closely when k is well below the number of threads.
+//     A histogram of the maxima gives that bound, the few elements above it go
+//     to one CTA, and it sorts them and settles the row.  Other k, and rows
+//     whose large elements crowd in few threads, take a histogram of all
+//     elements, and the crossing bin's elements are copied to every CTA, which
+//     settles the threshold among them.
+//   top-p: a histogram of counts, weighted with the bins' middles, estimates
+//     the bin of the cut.  One pass then computes every weight once and sums
+//     those above, in and below a window of a bin or two there, the window's
+//     elements copied to every CTA; the sums show the cut in the window, or,
+//     where the estimate was off, that a histogram of exact masses has to find
+//     it.
+// So a row takes two to four cluster barriers and at most one pass over its
+// weights; only long runs of ties take more rounds.
 #pragma once
 
 #include "q8q8_mma.cuh"
@@ -31,7 +40,9 @@ constexpr int kSampleWarps = kSampleThreads / 32;
 constexpr int kSampleBins = 2048;
 constexpr int kSampleGroup = 64;  // bins per group
 constexpr int kSampleGroups = kSampleBins / kSampleGroup;
-constexpr int kSampleList = 1024;
+constexpr int kSampleList = 1024;    // a count's or an exact mass's crossing bin
+constexpr int kSampleWindow = 2048;  // top-p's window
+constexpr int kSampleShortK = 256;   // largest top_k of the short path
 constexpr int kSampleMaxCluster = 16;
 constexpr int kSampleMaxSlice = 32768;  // logits per CTA
 constexpr double kSampleLive = 30.498476203173505;  // 44 ln 2: smaller weights are zero
@@ -52,29 +63,37 @@ struct SampleArgs {
 };
 
 // What the other CTAs of the cluster write here.
-struct SampleInbox {
-    u64 gmass[kSampleGroups];
+struct alignas(16) SampleInbox {
+    u64 gmass[kSampleGroups];      // a group's mass, or the bits of its fp32 estimate
     uint32_t gcnt[kSampleGroups];
-    u64 best;  // largest composite key
-    u64 kept;  // kept mass, or the mass above the crossing bin
+    u64 best;                      // largest composite key
+    u64 above, below, kept;        // masses of the pass over the weights
+    uint32_t sent;                 // elements of the short list
 };
 
-struct SampleShared {
-    u64 mass[kSampleBins];     // read by the cluster
-    uint32_t cnt[kSampleBins];
-    u64 list[kSampleList];     // written by the cluster
-    uint32_t list_n[2];        // entries given out (rank 0's counts for all), per filter
-    u64 wsum[kSampleWarps];
-    u64 gm[32];                // group sums of a list's histogram
+struct alignas(16) SampleShared {
+    // one of the two holds a list written by the cluster (top-p's window the
+    // first, the others the second), the other the histogram that settles it;
+    // the first is also the histogram of exact masses, read by the cluster,
+    // and the sort's exchange
+    u64 mass[kSampleBins];
+    u64 list[kSampleList];
+    uint32_t cnt[kSampleBins];  // read by the cluster
+    double tab[256];            // 2^(-j / 256)
+    u64 wsum[kSampleWarps], wabove[kSampleWarps], wbelow[kSampleWarps];
+    u64 gm[32];                 // group sums of a list's histogram
     u64 tiny[32];
     uint32_t tiny_n;
+    uint32_t sent;              // elements this CTA has put into a list
+    uint32_t short_n;           // rank 0: places of the short list given out
     // results of one thread or warp for the whole CTA
     u64 before, lo, hi, target, val;
     u64 tot[kSampleMaxCluster];
-    uint32_t count, above;
+    uint32_t count, above, base;
     int bin;
 };
 
+// (the logits that follow the inboxes are stored four at a time)
 __host__ __device__ inline size_t sample_smem_bytes(int slice, int cl) {
     return sizeof(SampleShared) + (size_t)cl * sizeof(SampleInbox) + (size_t)slice * 4;
 }
@@ -124,47 +143,43 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
-// Fixed-point weight of a logit (mx: the row's largest).  2^(-(k + r) / 32)
-// with k = round(32 log2(e) (mx - l) / T): a table of 2^(-j / 32) held one
-// entry per lane, and the Taylor polynomial of 2^(-r / 32) to the fifth power
-// (|r| <= 1/2: its remainder is below 2^-48), so 12 double operations.
-// Whole warps only; a weight below the live threshold comes out as garbage.
+// Fixed-point weight of a logit (mx: the row's largest).  2^(-(k + r) / 256)
+// with k = round(256 log2(e) (mx - l) / T): a table of 2^(-j / 256) and the
+// Taylor polynomial of 2^(-r / 256) to the fourth power (|r| <= 1/2: its
+// remainder is below 2^-53), so 11 double operations.  A weight below the live
+// threshold comes out as garbage.
 struct SampleWeight {
     float mx;
-    double c;    // 32 log2(e) / T
-    double tab;  // 2^(-lane / 32)
+    double c;           // 256 log2(e) / T
+    const double *tab;  // in shared memory
     __device__ __forceinline__ u64 operator()(float l) const {
         constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52
-        constexpr double a = 0.021660849392498290;     // ln 2 / 32
+        constexpr double a = 0.0027076061740622863;    // ln 2 / 256
         const double d = (double)mx - (double)l;
         const double t = __fma_rn(d, c, kMagic);
         const int k = __double2loint(t);
         const double r = __fma_rn(d, c, -(t - kMagic));
-        double p = __fma_rn(r, -a * a * a * a * a / 120, a * a * a * a / 24);
-        p = __fma_rn(r, p, -a * a * a / 6);
+        double p = __fma_rn(r, a * a * a * a / 24, -a * a * a / 6);
         p = __fma_rn(r, p, a * a / 2);
         p = __fma_rn(r, p, -a);
         p = __fma_rn(r, p, 1.0);
-        const double w = p * __shfl_sync(0xffffffffu, tab, k & 31);
-        const double s = __hiloint2double(__double2hiint(w) + ((43 - (k >> 5)) << 20), __double2loint(w));
+        const double w = p * tab[k & 255];
+        const double s = __hiloint2double(__double2hiint(w) + ((43 - (k >> 8)) << 20), __double2loint(w));
         const u64 f = (u64)__double_as_longlong(s + 4503599627370496.0) & 0xfffffffffffffull;  // + 2^52
         return l == mx ? 1ull << 43 : f;
     }
 };
 
-// The histogram's bins: 128 to a unit of (mx - l) / T down to 14, then 16 to a
-// unit, and the last bin takes what lies beyond.  Bin 0 holds the largest
-// logits and the bin never falls as the logit falls: every step is a monotone
-// fp32 operation, the conversion clamps, and it takes the NaN of inf - inf or
-// 0 * inf to bin 0.  (14 units below the top a token of 2^19 holds under one
-// part in 2^20 of the mass; finer bins above make the crossing bin's list
-// short.)
+// The histogram's bins: `scale` to a unit of mx - l, the last bin takes what
+// lies beyond.  Bin 0 holds the largest logits and the bin never falls as the
+// logit falls: every step is a monotone fp32 operation.  Adding 2^23 rounds to
+// an integer held in the low bits; the clamp takes the NaN of inf - inf or
+// 0 * inf to the last bin, where the row's other elements then are as well.
 struct SampleBinning {
-    float mx, scale;  // 128 / T
+    float mx, scale;
     __device__ __forceinline__ int operator()(float l) const {
-        const float v = __fmul_rn(__fsub_rn(mx, l), scale);
-        const float s = v < 1792.f ? v : __fadd_rn(1792.f, __fmul_rn(__fsub_rn(v, 1792.f), 0.125f));
-        return min(max(__float2int_rz(s), 0), kSampleBins - 1);
+        const float v = fminf(__fmaf_rn(__fsub_rn(mx, l), scale, 8388608.f), 8388608.f + (kSampleBins - 1));
+        return __float_as_int(v) & (kSampleBins - 1);
     }
 };
 
@@ -197,291 +212,383 @@ struct SampleRow {
     }
 };
 
-// Among the list's entries e >= kt, in descending order of e (by_index: in
-// ascending index order), the one where the running count (MASS: mass), from
-// `before`, reaches `target`: the only entries that can are those of order
-// keys [lo, hi], and one of them does.  Returns its order key (e, or its low
-// half).  Whole CTA.
+// 64-bit sum in shared memory as two 32-bit atomics with a carry (a 64-bit
+// atomicAdd on shared memory measured four times as long).
+__device__ __forceinline__ void add_mass(u64 *at, u64 w) {
+    uint32_t *p = reinterpret_cast<uint32_t *>(at);
+    const uint32_t lo = (uint32_t)w;
+    const uint32_t hi = (uint32_t)(w >> 32) + (atomicAdd(p, lo) + lo < lo ? 1u : 0u);
+    if (hi) atomicAdd(p + 1, hi);
+}
+
+// The list entry at which, in descending order, the running count (MASS: mass)
+// from `before` reaches `target`; with MASS and target 0 the target is top_p of
+// `other` and the list's mass together.  False when that does not lie in the
+// list.  Whole CTA.
 template <bool MASS>
-__device__ u64 sample_list_select(const SampleRow &s, int n, u64 kt, bool by_index, u64 lo, u64 hi, u64 before,
-                                  u64 target) {
+__device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 before, u64 target, double top_p, u64 other,
+                                   u64 *kt) {
     SampleShared &sh = *s.sh;
+    const u64 *list = window ? sh.mass : sh.list;
+    u64 *mass = window ? sh.list : sh.mass;  // 1024 bins
     uint32_t count = (uint32_t)n;
+    u64 lo = 0, hi = ~0ull;
+    bool first = true;
+    auto settle_target = [&](u64 all) {
+        if (MASS && target == 0) {
+            target = (u64)ceil(top_p * (double)(other + all));
+            if (target < 1) target = 1;
+        }
+    };
+    if (count > 32) {
+        u64 mn = ~0ull, mxv = 0;
+        for (int i = s.tid; i < n; i += kSampleThreads) {
+            const u64 e = list[i];
+            mn = min(mn, e);
+            mxv = max(mxv, e);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+            mxv = max(mxv, __shfl_xor_sync(0xffffffffu, mxv, off));
+        }
+        if (s.lane == 0) {
+            sh.gm[s.warp] = mn;
+            sh.gm[16 + s.warp] = mxv;
+        }
+        for (int i = s.tid; i < 1024; i += kSampleThreads) {
+            sh.cnt[i] = 0;
+            if (MASS) mass[i] = 0;
+        }
+        __syncthreads();
+        lo = sh.gm[0];
+        hi = sh.gm[16];
+#pragma unroll
+        for (int w = 1; w < kSampleWarps; ++w) {
+            lo = min(lo, sh.gm[w]);
+            hi = max(hi, sh.gm[16 + w]);
+        }
+        __syncthreads();
+    }
     while (count > 32) {
         const int bits = 64 - __clzll((long long)(hi - lo));
         const int shift = max(0, bits - 10);  // 1024 bins, 32 groups of 32
-        for (int i = s.tid; i < 1024; i += kSampleThreads) {
-            sh.cnt[i] = 0;
-            if (MASS) sh.mass[i] = 0;
+        if (!first) {
+            for (int i = s.tid; i < 1024; i += kSampleThreads) {
+                sh.cnt[i] = 0;
+                if (MASS) mass[i] = 0;
+            }
+            __syncthreads();
         }
-        __syncthreads();
-        for (int i = s.tid; i - s.lane < n; i += kSampleThreads) {
-            const u64 e = i < n ? sh.list[i] : 0;
-            const u64 o = by_index ? (uint32_t)e : e;
-            const u64 w = MASS ? s.weight(key_logit((uint32_t)(e >> 32))) : 0;
-            if (i < n && e >= kt && o >= lo && o <= hi) {
-                const int b = (int)((hi - o) >> shift);
+        for (int i = s.tid; i < n; i += kSampleThreads) {
+            const u64 e = list[i];
+            if (e >= lo && e <= hi) {
+                const int b = (int)((hi - e) >> shift);
                 atomicAdd(&sh.cnt[b], 1u);
-                if (MASS) atomicAdd(&sh.mass[b], w);
+                if (MASS) add_mass(&mass[b], s.weight(key_logit((uint32_t)(e >> 32))));
             }
         }
         __syncthreads();
-        for (int g = s.warp; g < 32; g += kSampleWarps) {
-            const u64 v = warp_sum(MASS ? sh.mass[g * 32 + s.lane] : (u64)sh.cnt[g * 32 + s.lane]);
-            if (s.lane == 0) sh.gm[g] = v;
+        {  // group sums, two groups of 32 bins a warp (two bins a lane)
+            const u64 v0 = MASS ? mass[2 * s.tid] + mass[2 * s.tid + 1] : (u64)sh.cnt[2 * s.tid] + sh.cnt[2 * s.tid + 1];
+            u64 v = v0;
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+            if ((s.lane & 15) == 0) sh.gm[s.tid >> 4] = v;
         }
         __syncthreads();
         if (s.warp == 0) {
             u64 v = sh.gm[s.lane];
             u64 inc = before + warp_incl_scan(v, s.lane);
-            const int g = __ffs(__ballot_sync(0xffffffffu, inc - v < target && target <= inc)) - 1;
-            const u64 b4 = __shfl_sync(0xffffffffu, inc - v, g);
-            const uint32_t c = sh.cnt[g * 32 + s.lane];
-            v = MASS ? sh.mass[g * 32 + s.lane] : c;
-            inc = b4 + warp_incl_scan(v, s.lane);
-            if (inc - v < target && target <= inc) {
-                const u64 top = hi - ((u64)(g * 32 + s.lane) << shift);
-                const u64 span = (1ull << shift) - 1;
-                sh.hi = top;
-                sh.lo = top - lo > span ? top - span : lo;
-                sh.before = inc - v;
-                sh.count = c;
+            if (first) settle_target(__shfl_sync(0xffffffffu, inc, 31) - before);
+            const unsigned cross = __ballot_sync(0xffffffffu, inc - v < target && target <= inc);
+            if (cross) {
+                const int g = __ffs(cross) - 1;
+                const u64 b4 = __shfl_sync(0xffffffffu, inc - v, g);
+                const uint32_t c = sh.cnt[g * 32 + s.lane];
+                v = MASS ? mass[g * 32 + s.lane] : c;
+                inc = b4 + warp_incl_scan(v, s.lane);
+                if (inc - v < target && target <= inc) {
+                    const u64 top = hi - ((u64)(g * 32 + s.lane) << shift);
+                    const u64 span = (1ull << shift) - 1;
+                    sh.hi = top;
+                    sh.lo = top - lo > span ? top - span : lo;
+                    sh.before = inc - v;
+                    sh.count = c;
+                    sh.target = target;
+                }
+            } else if (s.lane == 0) {
+                sh.count = 0;
             }
         }
         __syncthreads();
         lo = sh.lo;
         hi = sh.hi;
         before = sh.before;
+        target = sh.target;
         count = sh.count;
+        first = false;
         __syncthreads();
+        if (count == 0) return false;
     }
     if (s.tid == 0) sh.tiny_n = 0;
     __syncthreads();
     for (int i = s.tid; i < n; i += kSampleThreads) {
-        const u64 e = sh.list[i];
-        const u64 o = by_index ? (uint32_t)e : e;
-        if (e >= kt && o >= lo && o <= hi) sh.tiny[atomicAdd(&sh.tiny_n, 1u) & 31u] = e;
+        const u64 e = list[i];
+        if (e >= lo && e <= hi) sh.tiny[atomicAdd(&sh.tiny_n, 1u) & 31u] = e;
     }
     __syncthreads();
     if (s.warp == 0) {
         const int tn = min((int)sh.tiny_n, 32);
         const u64 e = s.lane < tn ? sh.tiny[s.lane] : 0;
-        const u64 o = by_index ? (uint32_t)e : e;
-        u64 w = MASS ? s.weight(key_logit((uint32_t)(e >> 32))) : 1;
-        if (s.lane >= tn) w = 0;
+        const u64 w = s.lane >= tn ? 0 : MASS ? s.weight(key_logit((uint32_t)(e >> 32))) : 1;
+        if (first) settle_target(warp_sum(w));
         u64 ex = before;
         for (int j = 0; j < tn; ++j) {
-            const u64 oj = __shfl_sync(0xffffffffu, o, j), wj = __shfl_sync(0xffffffffu, w, j);
-            if (oj > o) ex += wj;
+            const u64 ej = __shfl_sync(0xffffffffu, e, j), wj = __shfl_sync(0xffffffffu, w, j);
+            if (ej > e) ex += wj;
         }
-        if (s.lane < tn && ex < target && target <= ex + w) sh.val = o;
+        const bool here = s.lane < tn && ex < target && target <= ex + w;
+        if (here) sh.val = e;
+        const unsigned any = __ballot_sync(0xffffffffu, here);
+        if (s.lane == 0) sh.count = any;
     }
     __syncthreads();
-    const u64 r = sh.val;
-    __syncthreads();
-    return r;
+    *kt = sh.val;
+    return sh.count != 0;
 }
 
-// The mass of the list's entries e >= kt.  Whole CTA.
-__device__ u64 sample_list_mass(const SampleRow &s, int n, u64 kt) {
-    SampleShared &sh = *s.sh;
-    u64 m = 0;
-    for (int i = s.tid; i - s.lane < n; i += kSampleThreads) {
-        const u64 e = i < n ? sh.list[i] : 0;
-        const u64 w = s.weight(key_logit((uint32_t)(e >> 32)));
-        if (i < n && e >= kt) m += w;
-    }
-    m = warp_sum(m);
-    if (s.lane == 0) sh.wsum[s.warp] = m;
-    __syncthreads();
-    m = 0;
-    for (int w = 0; w < kSampleWarps; ++w) m += sh.wsum[w];
-    __syncthreads();
-    return m;
-}
-
-enum { kSampleWhole, kSampleShort, kSampleFound };
-
-// One filter: the threshold composite key in [lo, hi] of a count (the first
-// `target`) or, MASS, of a mass (top_p of the interval's).  Returns
-//   kSampleFound: *kt set, the same in every CTA (in_first: settled in the
-//     first histogram, whose per-CTA mass above the crossing bin is in
-//     inbox[].kept and whose list of n entries is still there);
-//   kSampleShort: the list holds every element that may be kept (n of them, in
-//     rank 0 only), [*blo, *bhi] the crossing bin's keys, *before and *target
-//     its sums; *bhi < *blo when the filter cuts nothing;
-//   kSampleWhole: the filter cuts nothing and the elements are many.
+// Histogram of the elements K in [lo, hi] (shift < 0: by the logit's bin, else
+// by digits of K), counts and with MASS masses.  Whole CTA.
 template <bool MASS>
-__device__ int sample_filter(const SampleRow &s, u64 lo, u64 hi, u64 target, double top_p, int slot, u64 *kt, int *n_list,
-                             u64 *blo, u64 *bhi, u64 *before_out, u64 *target_out, bool *in_first) {
+__device__ __forceinline__ void sample_histogram(const SampleRow &s, u64 lo, u64 hi, int shift) {
+    SampleShared &sh = *s.sh;
+    for (int i = s.tid; i < kSampleBins; i += kSampleThreads) {
+        sh.cnt[i] = 0;
+        if (MASS) sh.mass[i] = 0;
+    }
+    __syncthreads();
+    const uint32_t klo = (uint32_t)(lo >> 32);
+#pragma unroll 8
+    for (int i = s.tid; i < s.n; i += kSampleThreads) {
+        const float l = s.l[i];
+        if (logit_key(l) >= klo) {
+            const u64 k = s.composite(i);
+            if (k >= lo && k <= hi) {
+                const int b = shift < 0 ? s.bin(l) : (int)((hi - k) >> shift);
+                atomicAdd(&sh.cnt[b], 1u);
+                if (MASS) add_mass(&sh.mass[b], s.weight(l));
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// The group sums of this CTA's histogram to every CTA: counts, with masses
+// (MASS) or, est > 0, mass estimates exp2(-est * bin).  Four bins a thread, so
+// a group is half a warp, whose lanes then each write to one CTA.  Ends with a
+// cluster barrier.
+template <bool MASS>
+__device__ __forceinline__ void sample_share(const SampleRow &s, float est) {
+    SampleShared &sh = *s.sh;
+    static_assert(kSampleBins == 4 * kSampleThreads && kSampleGroup == 64 && kSampleMaxCluster == 16, "a thread's four bins");
+    const uint4 q = reinterpret_cast<const uint4 *>(sh.cnt)[s.tid];
+    uint32_t c = q.x + q.y + q.z + q.w;
+    u64 m = 0;
+    float e = 0.f;
+    if (MASS)
+        m = sh.mass[4 * s.tid] + sh.mass[4 * s.tid + 1] + sh.mass[4 * s.tid + 2] + sh.mass[4 * s.tid + 3];
+    else if (est > 0.f) {
+        const float b = 4.f * (float)s.tid;
+        e = (float)q.x * exp2f(-est * b) + (float)q.y * exp2f(-est * (b + 1.f)) + (float)q.z * exp2f(-est * (b + 2.f)) +
+            (float)q.w * exp2f(-est * (b + 3.f));
+    }
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) {
+        c += __shfl_xor_sync(0xffffffffu, c, off);
+        if (MASS) m += __shfl_xor_sync(0xffffffffu, m, off);
+        e += __shfl_xor_sync(0xffffffffu, e, off);
+    }
+    const uint32_t p = s.lane & 15, g = s.tid >> 4;
+    if (p < s.CL) {
+        const SampleInbox *box = &s.inbox[s.rank];
+        st_cluster_u32(map_to_rank(smem_u32(&box->gcnt[g]), p), c);
+        if (MASS || est > 0.f) st_cluster_u64(map_to_rank(smem_u32(&box->gmass[g]), p), MASS ? m : __float_as_uint(e));
+    }
+    cluster_sync_all();
+}
+
+// The counts of the 64 bins of group g (lane's bins: 64 g + lane and + 32), of
+// all CTAs and of those of lower rank.
+__device__ __forceinline__ void sample_pull_counts(const SampleRow &s, int g, uint32_t (&c)[2], uint32_t (&lower)[2]) {
+    c[0] = c[1] = lower[0] = lower[1] = 0;
+    uint32_t v[2][kSampleMaxCluster];
+#pragma unroll
+    for (uint32_t p = 0; p < kSampleMaxCluster; ++p) {
+        v[0][p] = v[1][p] = 0;
+        if (p < s.CL) {
+            const uint32_t a = map_to_rank(smem_u32(&s.sh->cnt[g * kSampleGroup + s.lane]), p);
+            v[0][p] = ld_cluster_u32(a);
+            v[1][p] = ld_cluster_u32(a + 128);
+        }
+    }
+#pragma unroll
+    for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            c[h] += v[h][p];
+            if (p < s.rank) lower[h] += v[h][p];
+        }
+}
+
+// One filter, exactly: the threshold composite key in [lo, hi] of a count (the
+// first `target`) or, MASS, of a mass (top_p of the interval's), the same in
+// every CTA.  False when the filter cuts nothing.
+template <bool MASS>
+__device__ bool sample_filter(const SampleRow &s, u64 lo, u64 hi, u64 target, double top_p, u64 *kt) {
     SampleShared &sh = *s.sh;
     u64 before = 0;
     for (int it = 0;; ++it) {
         const int bits = 64 - __clzll((long long)(hi - lo));
-        const int shift = max(0, bits - 11);  // later rounds: digits of the composite key
-        if (it > 0) cluster_sync_all();       // the histogram is no longer read
-        for (int i = s.tid; i < kSampleBins; i += kSampleThreads) {
-            sh.cnt[i] = 0;
-            if (MASS) sh.mass[i] = 0;
-        }
-        __syncthreads();
-#pragma unroll 4
-        for (int i = s.tid; i - s.lane < s.n; i += kSampleThreads) {
-            const float l = i < s.n ? s.l[i] : 0.f;
-            const u64 k = ((u64)logit_key(l) << 32) | (0xffffffffu - (uint32_t)(s.i0 + i));
-            const u64 w = MASS ? s.weight(l) : 0;
-            if (i < s.n && k >= lo && k <= hi) {
-                const int b = it == 0 ? s.bin(l) : (int)((hi - k) >> shift);
-                atomicAdd(&sh.cnt[b], 1u);
-                if (MASS) atomicAdd(&sh.mass[b], w);
-            }
-        }
-        __syncthreads();
-        for (int g = s.warp; g < kSampleGroups; g += kSampleWarps) {
-            const int b = g * kSampleGroup + s.lane;
-            const uint32_t c = warp_sum(sh.cnt[b] + sh.cnt[b + 32]);
-            const u64 m = MASS ? warp_sum(sh.mass[b] + sh.mass[b + 32]) : 0;
-            if (s.lane < (int)s.CL) {
-                st_cluster_u32(map_to_rank(smem_u32(&s.inbox[s.rank].gcnt[g]), s.lane), c);
-                if (MASS) st_cluster_u64(map_to_rank(smem_u32(&s.inbox[s.rank].gmass[g]), s.lane), m);
-            }
-        }
-        cluster_sync_all();
-        // the crossing group, then its bins from all CTAs (two warps, a bin a lane and warp)
-        if (s.warp < 2) {
+        const int shift = it == 0 ? -1 : max(0, bits - 11);  // later rounds: digits of the composite key
+        if (it > 0 || MASS) cluster_sync_all();              // the last histogram and its sums are no longer read
+        sample_histogram<MASS>(s, lo, hi, shift);
+        if (s.tid == 0) sh.sent = 0;
+        sample_share<MASS>(s, 0.f);
+        if (s.warp == 0) {  // the crossing group, then its bins from all CTAs
             u64 v = 0;
-            uint32_t c = 0;
-            for (uint32_t p = 0; p < s.CL; ++p) {
-                c += s.inbox[p].gcnt[s.lane];
-                if (MASS) v += s.inbox[p].gmass[s.lane];
-            }
-            if (!MASS) v = c;
+#pragma unroll
+            for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
+                if (p < s.CL) v += MASS ? s.inbox[p].gmass[s.lane] : s.inbox[p].gcnt[s.lane];
             const u64 inc = warp_incl_scan(v, s.lane);
-            const uint32_t cinc = warp_incl_scan(c, s.lane);
             const u64 all = __shfl_sync(0xffffffffu, inc, 31);
-            const uint32_t call = __shfl_sync(0xffffffffu, cinc, 31);
             if (MASS && it == 0) {
                 target = (u64)ceil(top_p * (double)all);
                 if (target < 1) target = 1;
             }
             int b = -1;
-            uint32_t bc = 0, ba = call;
+            uint32_t bc = 0, off = 0;
             u64 b4 = before + all;
             if (target <= before + all) {
                 const unsigned cross = __ballot_sync(0xffffffffu, before + inc - v < target && target <= before + inc);
                 const int g = __ffs(cross) - 1;
                 b4 = before + __shfl_sync(0xffffffffu, inc - v, g);
-                ba = __shfl_sync(0xffffffffu, cinc - c, g);
-                uint32_t fc[2] = {0, 0};
+                uint32_t fc[2], fl[2];
                 u64 fm[2] = {0, 0};
+                sample_pull_counts(s, g, fc, fl);
+                if (MASS) {
 #pragma unroll
-                for (uint32_t p = 0; p < kSampleMaxCluster; ++p) {
-                    if (p < s.CL) {
-                        const uint32_t ac = map_to_rank(smem_u32(&sh.cnt[g * kSampleGroup + s.lane]), p);
-                        fc[0] += ld_cluster_u32(ac);
-                        fc[1] += ld_cluster_u32(ac + 128);
-                        if (MASS) {
+                    for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
+                        if (p < s.CL) {
                             const uint32_t am = map_to_rank(smem_u32(&sh.mass[g * kSampleGroup + s.lane]), p);
                             fm[0] += ld_cluster_u64(am);
                             fm[1] += ld_cluster_u64(am + 256);
                         }
-                    }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const u64 x = MASS ? fm[h] : fc[h];
                     const u64 xi = b4 + warp_incl_scan(x, s.lane);
-                    const uint32_t ci = ba + warp_incl_scan(fc[h], s.lane);
                     const unsigned at = __ballot_sync(0xffffffffu, xi - x < target && target <= xi);
                     if (b < 0 && at) {
                         const int f = __ffs(at) - 1;
                         b = g * kSampleGroup + 32 * h + f;
                         bc = __shfl_sync(0xffffffffu, fc[h], f);
+                        off = __shfl_sync(0xffffffffu, fl[h], f);
                         b4 = __shfl_sync(0xffffffffu, xi - x, f);
-                        ba = __shfl_sync(0xffffffffu, ci - fc[h], f);
                     } else if (b < 0) {
                         b4 = __shfl_sync(0xffffffffu, xi, 31);
-                        ba = __shfl_sync(0xffffffffu, ci, 31);
                     }
                 }
-                // the bin's keys: warp 0 the least, warp 1 the largest
-                u64 k;
-                if (it > 0)
-                    k = s.warp == 0 ? (hi - lo >> shift > (u64)b ? hi - (((u64)b + 1) << shift) + 1 : lo)
-                                    : hi - ((u64)b << shift);
-                else if (s.warp == 0)
-                    k = max(lo, least_key_of_bin(s.bin, (uint32_t)(lo >> 32), (uint32_t)(hi >> 32), b, s.lane) << 32);
-                else
-                    k = b == 0 ? hi
-                               : min(hi, (least_key_of_bin(s.bin, (uint32_t)(lo >> 32), (uint32_t)(hi >> 32), b - 1, s.lane)
-                                          << 32) - 1);
-                if (s.lane == 0) (s.warp == 0 ? sh.lo : sh.hi) = k;
+                if (it > 0 || bc > kSampleList) {  // the bin's keys
+                    const uint32_t l32 = (uint32_t)(lo >> 32), h32 = (uint32_t)(hi >> 32);
+                    u64 kl, kh;
+                    if (it > 0) {
+                        kl = (hi - lo) >> shift > (u64)b ? hi - (((u64)b + 1) << shift) + 1 : lo;
+                        kh = hi - ((u64)b << shift);
+                    } else {
+                        kl = max(lo, least_key_of_bin(s.bin, l32, h32, b, s.lane) << 32);
+                        kh = b == 0 ? hi : min(hi, (least_key_of_bin(s.bin, l32, h32, b - 1, s.lane) << 32) - 1);
+                    }
+                    if (s.lane == 0) {
+                        sh.lo = kl;
+                        sh.hi = kh;
+                    }
+                }
             }
-            if (s.tid == 0) {
+            if (s.lane == 0) {
                 sh.bin = b;
                 sh.count = bc;
-                sh.above = ba;
+                sh.base = off;
                 sh.before = b4;
                 sh.target = target;
             }
         }
         __syncthreads();
         const int b = sh.bin;
-        const uint32_t bc = sh.count, ba = sh.above;
-        const u64 nlo = b < 0 ? lo : sh.lo, nhi = b < 0 ? 0 : sh.hi;
+        if (b < 0) return false;
+        const uint32_t bc = sh.count, base = sh.base;
         before = sh.before;
         target = sh.target;
-        const bool all_short = it == 0 && ba + bc <= kSampleList;
-        if (b < 0 && !all_short) {
-            cluster_sync_all();  // the inbox is no longer read
-            return kSampleWhole;
-        }
-        if (all_short || bc <= kSampleList) {
-            // mass above the crossing bin, for the owner search
-            if (MASS && it == 0 && !all_short) {
-                u64 m = 0;
-                for (int i = s.tid; i < b; i += kSampleThreads) m += sh.mass[i];
-                m = warp_sum(m);
-                if (s.lane == 0) sh.wsum[s.warp] = m;
-                __syncthreads();
-                if (s.tid < (int)s.CL) {
-                    m = 0;
-                    for (int w = 0; w < kSampleWarps; ++w) m += sh.wsum[w];
-                    st_cluster_u64(map_to_rank(smem_u32(&s.inbox[s.rank].kept), s.tid), m);
-                }
-            }
-            const u64 from = nlo, to = all_short ? hi : nhi;
-            const uint32_t counter = map_to_rank(smem_u32(&sh.list_n[slot]), 0);
+        const u64 nlo = sh.lo, nhi = sh.hi;  // (set when it > 0 or bc > kSampleList)
+        if (bc <= kSampleList) {
 #pragma unroll 4
-            for (int i = s.tid; i - s.lane < s.n; i += kSampleThreads) {
-                const u64 k = i < s.n ? s.composite(i) : 0;
-                const bool in = i < s.n && k >= from && k <= to;
-                const unsigned m = __ballot_sync(0xffffffffu, in);
-                if (m) {
-                    uint32_t at = 0;
-                    if (s.lane == 0) at = atom_cluster_add(counter, (uint32_t)__popc(m));
-                    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << s.lane) - 1));
-                    if (in && at < kSampleList) {
-                        const uint32_t a = smem_u32(&sh.list[at]);
-                        for (uint32_t p = 0; p < (all_short ? 1u : s.CL); ++p) st_cluster_u64(map_to_rank(a, p), k);
-                    }
+            for (int i = s.tid; i < s.n; i += kSampleThreads) {
+                const u64 k = s.composite(i);
+                const bool in = it > 0 ? k >= nlo && k <= nhi : k >= lo && k <= hi && s.bin(s.l[i]) == b;
+                if (in) {
+                    const uint32_t at = base + atomicAdd(&sh.sent, 1u);
+                    if (at < kSampleList)
+                        for (uint32_t p = 0; p < s.CL; ++p) st_cluster_u64(map_to_rank(smem_u32(&sh.list[at]), p), k);
                 }
             }
             cluster_sync_all();
-            *n_list = (int)(all_short ? ba + bc : bc);
-            *blo = nlo;
-            *bhi = nhi;
-            *before_out = before;
-            *target_out = target;
-            if (all_short) return kSampleShort;
-            *kt = sample_list_select<MASS>(s, (int)bc, 0, false, nlo, nhi, before, target);
-            *in_first = it == 0;
-            return kSampleFound;
+            sample_list_select<MASS>(s, false, (int)bc, before, target, 0.0, 0, kt);
+            return true;
         }
         lo = nlo;
         hi = nhi;
         __syncthreads();
     }
+}
+
+// Descending bitonic sort of one value a thread over the first `width` threads
+// (a power of two, 32 .. kSampleThreads).  Whole CTA.
+__device__ __forceinline__ u64 sample_sort(const SampleRow &s, u64 v, int width) {
+    u64 *x = s.sh->mass;
+    int flip = 0;
+    for (int k = 2; k <= width; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            u64 o;
+            if (j >= 32) {  // two buffers in turn, so one barrier a step
+                x[flip + s.tid] = v;
+                __syncthreads();
+                o = x[flip + (s.tid ^ j)];
+                flip ^= kSampleThreads;
+            } else {
+                o = __shfl_xor_sync(0xffffffffu, v, j);
+            }
+            const bool big = ((s.tid & k) == 0) == ((s.tid & j) == 0);
+            v = (o > v) == big ? o : v;
+        }
+    return v;
+}
+
+// Inclusive sum over the threads, and the total.  Whole CTA.
+__device__ __forceinline__ u64 sample_scan(const SampleRow &s, u64 v, u64 *all) {
+    const u64 inc = warp_incl_scan(v, s.lane);
+    __syncthreads();
+    if (s.lane == 31) s.sh->wsum[s.warp] = inc;
+    __syncthreads();
+    u64 b4 = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kSampleWarps; ++w) {
+        const u64 x = s.sh->wsum[w];
+        if (w < s.warp) b4 += x;
+        sum += x;
+    }
+    *all = sum;
+    return b4 + inc;
 }
 
 __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleArgs a) {
@@ -497,7 +604,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     const int tid = s.tid = threadIdx.x, warp = s.warp = tid >> 5, lane = s.lane = tid & 31;
     const uint32_t CL = s.CL, rank = s.rank;
     const int row = blockIdx.x / CL;
-    if (tid < 2) sh.list_n[tid] = 0;
+    if (tid == 0) sh.short_n = sh.sent = 0;
     pdl_wait_and_trigger();
 
     // this CTA's logits: NaN counts as -inf, -0 as +0; the largest, lowest index first
@@ -505,143 +612,341 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     const int n = s.n = min(a.V, i0 + a.slice) - i0;
     const float *src = a.logits + (int64_t)row * a.ld + i0;
     u64 best = 0;
+    {
+        float mv = -INFINITY;
+        int mi = 0x7fffffff;
+        auto take = [&](float v, int i) {
+            v += 0.f;
+            if (!(v >= -INFINITY)) v = -INFINITY;
+            if (v > mv || mi == 0x7fffffff) {
+                mv = v;
+                mi = i;
+            }
+            return v;
+        };
+        if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+            const int n4 = n >> 2;
+#pragma unroll 4
+            for (int j = tid; j < n4; j += kSampleThreads) {
+                float4 q = __ldg(reinterpret_cast<const float4 *>(src) + j);
+                q.x = take(q.x, 4 * j);
+                q.y = take(q.y, 4 * j + 1);
+                q.z = take(q.z, 4 * j + 2);
+                q.w = take(q.w, 4 * j + 3);
+                reinterpret_cast<float4 *>(buf)[j] = q;
+            }
+            for (int i = 4 * n4 + tid; i < n; i += kSampleThreads) buf[i] = take(__ldg(src + i), i);
+        } else {
 #pragma unroll 8
-    for (int i = tid; i < n; i += kSampleThreads) {
-        float v = __ldg(src + i) + 0.f;
-        if (isnan(v)) v = -INFINITY;
-        buf[i] = v;
-        const u64 k = ((u64)logit_key(v) << 32) | (0xffffffffu - (uint32_t)(i0 + i));
-        best = k > best ? k : best;
+            for (int i = tid; i < n; i += kSampleThreads) buf[i] = take(__ldg(src + i), i);
+        }
+        if (mi != 0x7fffffff) best = ((u64)logit_key(mv) << 32) | (0xffffffffu - (uint32_t)(i0 + mi));
     }
+    const u64 own = best;  // this thread's largest
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const u64 o = __shfl_xor_sync(0xffffffffu, best, off);
-        best = o > best ? o : best;
-    }
+    for (int off = 16; off > 0; off >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, off));
     if (lane == 0) sh.wsum[warp] = best;
     __syncthreads();
     if (tid < (int)CL) {
         best = sh.wsum[0];
-        for (int w = 1; w < kSampleWarps; ++w) best = sh.wsum[w] > best ? sh.wsum[w] : best;
+#pragma unroll
+        for (int w = 1; w < kSampleWarps; ++w) best = max(best, sh.wsum[w]);
         st_cluster_u64(map_to_rank(smem_u32(&s.inbox[rank].best), tid), best);
     }
-    cluster_sync_all();
-    best = s.inbox[0].best;
-    for (uint32_t p = 1; p < CL; ++p) best = s.inbox[p].best > best ? s.inbox[p].best : best;
-    const float mx = key_logit((uint32_t)(best >> 32));
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // the row's parameters, while the barrier completes
     float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
-    if (mx == -INFINITY || !(temp > 0.f)) {  // nothing to draw from, or greedy
+    const bool greedy = !(temp > 0.f);
+    temp = fminf(temp, 3.402823466e38f);
+    const double t64 = temp;
+    const int top_k = a.top_k ? __ldg(a.top_k + row) : 0;
+    const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
+    const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
+    float u = __ldg(a.u + row);
+    u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
+    if (tid < 256) sh.tab[tid] = exp2(-tid / 256.0);
+    for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.cnt[i] = 0;
+    s.weight.c = 369.32993046757466 / t64;  // 256 log2(e)
+    s.weight.tab = sh.tab;
+    const double min_log = min_p > 0.f ? t64 * log((double)fminf(min_p, 1.f)) : 0.0;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    best = s.inbox[0].best;
+#pragma unroll
+    for (uint32_t p = 1; p < kSampleMaxCluster; ++p)
+        if (p < CL) best = max(best, s.inbox[p].best);
+    const uint32_t key_max = (uint32_t)(best >> 32);
+    const float mx = key_logit(key_max);
+    if (mx == -INFINITY || greedy) {  // nothing to draw from, or greedy
         if (rank == 0 && tid == 0) {
             a.token[row] = mx == -INFINITY ? -1 : (int32_t)(0xffffffffu - (uint32_t)best);
             if (a.prob) a.prob[row] = mx == -INFINITY ? 0.f : 1.f;
         }
         return;  // the whole cluster
     }
-    temp = fminf(temp, 3.402823466e38f);
-    s.weight = SampleWeight{mx, 46.166241308446828 / (double)temp, exp2(-lane / 32.0)};  // 32 log2(e)
-    s.bin = SampleBinning{mx, (float)(128.0 / (double)temp)};
+    s.weight.mx = s.bin.mx = mx;
 
     // threshold: the weight's cut-off, then each filter raises it
-    u64 kt = max(logit_key(__double2float_ru((double)mx - kSampleLive * (double)temp) + 0.f),
-                 logit_key(-3.402823466e38f));
+    u64 kt = max(logit_key(__double2float_ru((double)mx - kSampleLive * t64) + 0.f), logit_key(-3.402823466e38f));
     kt <<= 32;
     u64 kmin = 0;
-    const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
-    if (min_p > 0.f) {
-        const double c = (double)mx + (double)temp * log((double)fminf(min_p, 1.f));
-        kmin = (u64)min((uint32_t)(best >> 32), logit_key(__double2float_ru(c) + 0.f)) << 32;
-    }
-    const int top_k = a.top_k ? __ldg(a.top_k + row) : 0;
-    const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
-    float u = __ldg(a.u + row);
-    u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
+    if (min_p > 0.f) kmin = (u64)min(key_max, logit_key(__double2float_ru((double)mx + min_log) + 0.f)) << 32;
 
-    int n_list = 0, is = kSampleWhole;
-    u64 blo, bhi, before, target;
-    bool in_first = false, by_mass = false;
-    if (top_k > 0 && top_k < a.V) {
-        is = sample_filter<false>(s, kt, best, (u64)top_k, 0.0, 0, &kt, &n_list, &blo, &bhi, &before, &target, &in_first);
-        in_first = false;
-    }
-    if (top_p < 1.f && is != kSampleShort) {
-        is = sample_filter<true>(s, kt, best, 0, (double)top_p, 1, &kt, &n_list, &blo, &bhi, &before, &target, &in_first);
-        by_mass = true;
-    }
-
-    if (is == kSampleShort) {  // rank 0 settles the row from its list
-        if (rank != 0) return;
-        if (bhi >= blo) kt = by_mass ? sample_list_select<true>(s, n_list, kt, false, blo, bhi, before, target)
-                                     : sample_list_select<false>(s, n_list, kt, false, blo, bhi, before, target);
-        if (!by_mass && top_p < 1.f) {
-            const u64 z = sample_list_mass(s, n_list, kt);
-            target = (u64)ceil((double)top_p * (double)z);
-            kt = sample_list_select<true>(s, n_list, kt, false, kt, best, 0, target < 1 ? 1 : target);
-        }
-        kt = max(kt, kmin);
-        const u64 z = sample_list_mass(s, n_list, kt);
-        u64 r = (u64)((double)u * (double)z);
-        if (r > z - 1) r = z - 1;
-        const u64 o = sample_list_select<true>(s, n_list, kt, true, 0xffffffffu - (uint32_t)a.V, 0xffffffffu, 0, r + 1);
-        for (int i = tid; i < n_list; i += kSampleThreads)
-            if ((uint32_t)sh.list[i] == (uint32_t)o) {
-                const double d = (double)key_logit((uint32_t)(sh.list[i] >> 32)) - (double)mx;
-                a.token[row] = (int32_t)(0xffffffffu - (uint32_t)o);
-                if (a.prob) a.prob[row] = (float)((d == 0.0 || isnan(d) ? 1.0 : exp(d / (double)temp)) * 8796093022208.0 / (double)z);
-            }
-        return;
-    }
-
-    // kept mass of every CTA
-    const int seg = ((a.slice + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32;  // a warp's contiguous part
-    const int s0 = min(n, warp * seg), s1 = min(n, s0 + seg);
-    const bool known = in_first && kmin <= kt;  // the histogram's sums above the crossing bin, and the list's kept part
-    if (!known) kt = max(kt, kmin);
-    auto warp_masses = [&]() {
-        u64 m = 0;
-#pragma unroll 4
-        for (int i = s0 + lane; i - lane < s1; i += 32) {
-            const float l = i < s1 ? buf[i] : 0.f;
-            const u64 w = s.weight(l);
-            if (i < s1 && s.composite(i) >= kt) m += w;
-        }
-        m = warp_sum(m);
-        if (lane == 0) sh.wsum[warp] = m;
-        __syncthreads();
+    auto write = [&](uint32_t index, float l, u64 z) {
+        const double w = l == mx ? 1.0 : exp(((double)l - (double)mx) / t64);
+        a.token[row] = (int32_t)index;
+        if (a.prob) a.prob[row] = (float)(w * 8796093022208.0 / (double)z);  // 2^43
     };
-    if (known) {
-        if (tid < (int)CL) sh.tot[tid] = s.inbox[tid].kept;
-        __syncthreads();
-        for (int i = tid; i - lane < n_list; i += kSampleThreads) {
-            const u64 e = i < n_list ? sh.list[i] : 0;
-            const u64 w = s.weight(key_logit((uint32_t)(e >> 32)));
-            if (i < n_list && e >= kt) atomicAdd(&sh.tot[(0xffffffffu - (uint32_t)e) / (uint32_t)a.slice], w);
+
+    if (top_k > 0 && top_k < a.V) {
+        s.bin.scale = (float)(kSampleBins / kSampleLive / t64);  // bins over the whole live range
+        if (top_k <= kSampleShortK && top_k * 4 <= (int)CL * kSampleThreads) {
+            __syncthreads();
+            if (own >= kt) atomicAdd(&sh.cnt[s.bin(key_logit((uint32_t)(own >> 32)))], 1u);
+            __syncthreads();
+            sample_share<false>(s, 0.f);
+            if (warp == 0) {  // the bin of the k-th largest maximum, the last bin when there are fewer
+                uint32_t c = 0;
+#pragma unroll
+                for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
+                    if (p < CL) c += s.inbox[p].gcnt[lane];
+                const uint32_t inc = warp_incl_scan(c, lane);
+                const unsigned cross = __ballot_sync(0xffffffffu, inc >= (uint32_t)top_k);
+                int b = kSampleBins - 1;
+                if (cross) {
+                    const int g = __ffs(cross) - 1;
+                    uint32_t fc[2], unused[2];
+                    sample_pull_counts(s, g, fc, unused);
+                    const uint32_t c0 = __shfl_sync(0xffffffffu, inc - c, g) + warp_incl_scan(fc[0], lane);
+                    const uint32_t c1 = __shfl_sync(0xffffffffu, c0, 31) + warp_incl_scan(fc[1], lane);
+                    const unsigned at0 = __ballot_sync(0xffffffffu, c0 >= (uint32_t)top_k);
+                    const unsigned at1 = __ballot_sync(0xffffffffu, c1 >= (uint32_t)top_k);
+                    b = g * kSampleGroup + (at0 ? __ffs(at0) - 1 : 31 + __ffs(at1));
+                }
+                if (lane == 0) sh.bin = b;
+            }
+            __syncthreads();
+            // the elements down to that bin: gathered here, then sent to rank 0
+            const int b = sh.bin;
+            const uint32_t klo = (uint32_t)(kt >> 32);
+#pragma unroll 8
+            for (int i = tid; i < n; i += kSampleThreads) {
+                const float l = buf[i];
+                if (s.bin(l) <= b && logit_key(l) >= klo) {
+                    const uint32_t at = atomicAdd(&sh.sent, 1u);
+                    if (at < kSampleThreads) sh.mass[at] = s.composite(i);
+                }
+            }
+            __syncthreads();
+            const uint32_t sent = sh.sent;
+            if (tid == 0 && sent) sh.base = atom_cluster_add(map_to_rank(smem_u32(&sh.short_n), 0), sent);
+            if (tid < (int)CL) st_cluster_u32(map_to_rank(smem_u32(&s.inbox[rank].sent), tid), sent);
+            __syncthreads();
+            if (tid < (int)sent && sh.base + tid < kSampleThreads)
+                st_cluster_u64(map_to_rank(smem_u32(&sh.list[sh.base + tid]), 0), sh.mass[tid]);
+            cluster_sync_all();
+            uint32_t all = 0;
+            for (uint32_t p = 0; p < CL; ++p) all += s.inbox[p].sent;
+            if (all <= kSampleThreads) {  // rank 0 settles the row
+                if (rank != 0) return;
+                int width = 32;
+                while (width < (int)all) width *= 2;
+                // in the filters' order: top-k, top-p, min-p
+                const u64 e = sample_sort(s, tid < (int)all ? sh.list[tid] : 0, width);
+                const float l = key_logit((uint32_t)(e >> 32));
+                bool keep = tid < min((int)all, top_k);
+                u64 w = keep ? s.weight(l) : 0, z;
+                if (top_p < 1.f) {
+                    const u64 inc = sample_scan(s, w, &z);
+                    const u64 target = (u64)ceil((double)top_p * (double)z);
+                    keep = keep && inc - w < (target < 1 ? 1 : target);
+                }
+                keep = keep && e >= kmin;
+                // in index order: index and weight in one word (19 and 44 bits)
+                const uint32_t index = 0xffffffffu - (uint32_t)e;
+                const u64 y = sample_sort(s, keep ? ~((u64)index << 44 | w) : 0, width);
+                w = tid < width && y ? ~y & 0xfffffffffffull : 0;
+                const u64 inc = sample_scan(s, w, &z);
+                u64 r = (u64)((double)u * (double)z);
+                if (r > z - 1) r = z - 1;
+                if (inc - w <= r && r < inc) sh.base = (uint32_t)(~y >> 44);
+                __syncthreads();
+                if (keep && index == sh.base) write(index, l, z);
+                return;
+            }
+            __syncthreads();
+        }
+        if (!sample_filter<false>(s, kt, best, (u64)top_k, 0.0, &kt))
+            cluster_sync_all();  // the histogram's sums are no longer read
+    }
+
+    // one pass over the weights: a warp takes a contiguous part of the slice
+    const int seg = ((a.slice + kSampleWarps - 1) / kSampleWarps + 31) / 32 * 32;
+    const int s0 = min(n, warp * seg), s1 = min(n, s0 + seg);
+    const bool filter_p = top_p < 1.f;
+    int w0 = kSampleBins, w1 = -1;  // window of bins
+    uint32_t n_list = 0;
+    if (filter_p) {
+        // 128 bins to a unit: narrow where top-p cuts; they end 16 units down,
+        // and a cut below that takes the exact histogram
+        s.bin.scale = (float)(128.0 / t64);
+        constexpr float kEst = 1.4426950408889634f / 128.f;
+        sample_histogram<false>(s, kt, best, -1);
+        if (tid == 0) sh.sent = 0;
+        sample_share<false>(s, kEst);
+        if (warp == 0) {
+            float e = 0.f;
+            uint32_t c = 0, low = 0;
+#pragma unroll
+            for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
+                if (p < CL) {
+                    e += __uint_as_float((uint32_t)s.inbox[p].gmass[lane]);
+                    c += s.inbox[p].gcnt[lane];
+                    if (p < rank) low += s.inbox[p].gcnt[lane];
+                }
+            const float inc = warp_incl_scan(e, lane);
+            const uint32_t cinc = warp_incl_scan(c, lane);
+            const float goal = top_p * __shfl_sync(0xffffffffu, inc, 31);
+            const unsigned cross = __ballot_sync(0xffffffffu, inc >= goal);
+            const int g = cross ? __ffs(cross) - 1 : kSampleGroups - 1;
+            float b4 = __shfl_sync(0xffffffffu, inc - e, g);
+            const uint32_t ca = __shfl_sync(0xffffffffu, cinc - c, g);
+            const uint32_t la = __shfl_sync(0xffffffffu, warp_incl_scan(low, lane) - low, g);
+            uint32_t fc[2], fl[2];
+            sample_pull_counts(s, g, fc, fl);
+            const int base = g * kSampleGroup;
+            const float e0 = b4 + warp_incl_scan((float)fc[0] * exp2f(-kEst * (float)(base + lane)), lane);
+            const float e1 = __shfl_sync(0xffffffffu, e0, 31) +
+                             warp_incl_scan((float)fc[1] * exp2f(-kEst * (float)(base + 32 + lane)), lane);
+            const uint32_t c0 = ca + warp_incl_scan(fc[0], lane);
+            const uint32_t c1 = __shfl_sync(0xffffffffu, c0, 31) + warp_incl_scan(fc[1], lane);
+            const uint32_t l0 = warp_incl_scan(fl[0], lane);
+            const uint32_t l1 = __shfl_sync(0xffffffffu, l0, 31) + warp_incl_scan(fl[1], lane);
+            const unsigned at0 = __ballot_sync(0xffffffffu, e0 >= goal), at1 = __ballot_sync(0xffffffffu, e1 >= goal);
+            const int f = at0 ? __ffs(at0) - 1 : at1 ? 31 + __ffs(at1) : kSampleGroup - 1;
+            // the estimate's bin, with the neighbour that it lies close to, within
+            // the group; from the top when that is a short list
+            const float ef = (float)__shfl_sync(0xffffffffu, f < 32 ? fc[0] : fc[1], f & 31) * exp2f(-kEst * (float)(base + f));
+            const float part = (__shfl_sync(0xffffffffu, f < 32 ? e0 : e1, f & 31) - goal) / ef;  // of the bin, below the cut
+            const int f1 = part < 0.05f ? min(f + 1, kSampleGroup - 1) : f, f0 = part > 0.95f ? max(f - 1, 0) : f;
+            const uint32_t upto = __shfl_sync(0xffffffffu, f1 < 32 ? c0 : c1, f1 & 31);
+            const uint32_t lower = __shfl_sync(0xffffffffu, f1 < 32 ? l0 : l1, f1 & 31);
+            const uint32_t over = f0 == 0 ? ca : __shfl_sync(0xffffffffu, f0 <= 32 ? c0 : c1, (f0 - 1) & 31);
+            const uint32_t lover = f0 == 0 ? 0 : __shfl_sync(0xffffffffu, f0 <= 32 ? l0 : l1, (f0 - 1) & 31);
+            if (lane == 0) {
+                sh.bin = upto <= kSampleWindow ? 0 : base + f0;
+                sh.count = base + f1;
+                sh.above = upto <= kSampleWindow ? upto : upto - over;
+                sh.base = upto <= kSampleWindow ? la + lower : lower - lover;
+            }
         }
         __syncthreads();
-    } else {
-        warp_masses();
+        w0 = sh.bin;
+        w1 = (int)sh.count;
+        n_list = sh.above;
+        if (n_list > kSampleWindow) w1 = -1;  // no list: the exact histogram
+    }
+    auto masses = [&](u64 thr, bool window) {
+        u64 ma = 0, mb = 0, mk = 0;
+        const uint32_t klo = (uint32_t)((window ? kt : thr) >> 32);
+        const uint32_t base = sh.base;
+#pragma unroll 4
+        for (int i = s0 + lane; i < s1; i += 32) {
+            const float l = buf[i];
+            if (logit_key(l) < klo) continue;
+            const u64 k = s.composite(i);
+            const u64 w = s.weight(l);
+            if (k >= thr) mk += w;
+            if (window && k >= kt) {
+                const int b = s.bin(l);
+                if (b < w0)
+                    ma += w;
+                else if (b > w1)
+                    mb += w;
+                else {
+                    const uint32_t at = base + atomicAdd(&sh.sent, 1u);
+                    if (at < kSampleWindow)
+                        for (uint32_t p = 0; p < CL; ++p) st_cluster_u64(map_to_rank(smem_u32(&sh.mass[at]), p), k);
+                }
+            }
+        }
+        mk = warp_sum(mk);
+        if (window) {
+            ma = warp_sum(ma);
+            mb = warp_sum(mb);
+        }
+        __syncthreads();
+        if (lane == 0) {
+            sh.wsum[warp] = mk;
+            sh.wabove[warp] = ma;
+            sh.wbelow[warp] = mb;
+        }
+        __syncthreads();
         if (tid < (int)CL) {
-            u64 m = 0;
-            for (int w = 0; w < kSampleWarps; ++w) m += sh.wsum[w];
-            st_cluster_u64(map_to_rank(smem_u32(&s.inbox[rank].kept), tid), m);
+            mk = ma = mb = 0;
+#pragma unroll
+            for (int w = 0; w < kSampleWarps; ++w) {
+                mk += sh.wsum[w];
+                ma += sh.wabove[w];
+                mb += sh.wbelow[w];
+            }
+            const uint32_t box = smem_u32(&s.inbox[rank]);
+            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, kept), tid), mk);
+            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, above), tid), ma);
+            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, below), tid), mb);
         }
         cluster_sync_all();
-        if (tid < (int)CL) sh.tot[tid] = s.inbox[tid].kept;
+    };
+    // the sums over K >= thr where top-p is off, or min-p's own threshold turns out above top-p's
+    u64 thr = max(kt, kmin);
+    bool listed = false;  // the kept mass is that above the window and the list's kept part
+    if (!filter_p || w1 >= 0) masses(thr, w1 >= 0);
+    if (filter_p) {
+        bool found = false;
+        if (w1 >= 0) {
+            u64 above = 0, z = 0;
+#pragma unroll
+            for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
+                if (p < CL) {
+                    above += s.inbox[p].above;
+                    z += s.inbox[p].below;
+                }
+            u64 cut;
+            found = sample_list_select<true>(s, true, (int)n_list, above, 0, (double)top_p, above + z, &cut);
+            if (found) kt = cut;
+        }
+        if (!found) {
+            sample_filter<true>(s, kt, best, 0, (double)top_p, &kt);
+            thr = max(kt, kmin);
+            masses(thr, false);
+        } else if (kt >= kmin) {
+            listed = true;
+            thr = kt;
+        }
+    }
+    // kept mass of every CTA and of this one's warps
+    if (tid < (int)CL) sh.tot[tid] = listed ? s.inbox[tid].above : s.inbox[tid].kept;
+    if (listed && tid < kSampleWarps) sh.wsum[tid] = sh.wabove[tid];
+    __syncthreads();
+    if (listed) {
+        for (int i = tid; i < (int)n_list; i += kSampleThreads) {
+            const u64 e = sh.mass[i];  // the window's list
+            if (e >= kt) {
+                const u64 w = s.weight(key_logit((uint32_t)(e >> 32)));
+                const uint32_t at = 0xffffffffu - (uint32_t)e, p = at / (uint32_t)a.slice;
+                add_mass(&sh.tot[p], w);
+                if (p == rank) add_mass(&sh.wsum[(at - i0) / seg], w);
+            }
+        }
         __syncthreads();
     }
     // the CTA that the uniform number falls into goes on alone
-    u64 z = 0, r = 0;
-    {
-        for (uint32_t p = 0; p < CL; ++p) z += sh.tot[p];
-        r = (u64)((double)u * (double)z);
-        if (r > z - 1) r = z - 1;
-        uint32_t p = 0;
-        while (p < CL && r >= sh.tot[p]) r -= sh.tot[p++];
-        if (p != rank) return;
-    }
-    if (known) {
-        __syncthreads();
-        warp_masses();
-    }
+    u64 z = 0;
+    for (uint32_t p = 0; p < CL; ++p) z += sh.tot[p];
+    u64 r = (u64)((double)u * (double)z);
+    if (r > z - 1) r = z - 1;
+    uint32_t owner = 0;
+    while (owner < CL - 1 && r >= sh.tot[owner]) r -= sh.tot[owner++];
+    if (owner != rank) return;
     int part = 0;  // the warp's part it falls into
     while (part < kSampleWarps - 1 && r >= sh.wsum[part]) r -= sh.wsum[part++];
     __syncthreads();
@@ -649,31 +954,19 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     const int e0 = part * seg + tid * per;
     const int e1 = min(min(n, (part + 1) * seg), e0 + per);
     u64 m = 0;
-    for (int j = 0; j < per; ++j) {
-        const int i = e0 + j;
-        const float l = i < e1 ? buf[i] : 0.f;
-        const u64 w = s.weight(l);
-        if (i < e1 && s.composite(i) >= kt) m += w;
-    }
+    for (int i = e0; i < e1; ++i)
+        if (s.composite(i) >= thr) m += s.weight(buf[i]);
     u64 inc = warp_incl_scan(m, lane);
     if (lane == 31) sh.wsum[warp] = inc;
     __syncthreads();
     for (int w = 0; w < warp; ++w) inc += sh.wsum[w];
     u64 run = inc - m;
-    const bool mine = run <= r && r < inc;
-    if (!__ballot_sync(0xffffffffu, mine)) return;
-    for (int j = 0; j < per; ++j) {
-        const int i = e0 + j;
-        const float l = i < e1 ? buf[i] : 0.f;
-        u64 w = s.weight(l);
-        if (!(i < e1 && s.composite(i) >= kt)) w = 0;
-        if (mine && run <= r && r < run + w) {
-            const double d = (double)l - (double)mx;
-            a.token[row] = i0 + i;
-            if (a.prob) a.prob[row] = (float)((l == mx ? 1.0 : exp(d / (double)temp)) * 8796093022208.0 / (double)z);
+    if (run <= r && r < inc)
+        for (int i = e0; i < e1; ++i) {
+            const u64 w = s.composite(i) >= thr ? s.weight(buf[i]) : 0;
+            if (run <= r && r < run + w) write((uint32_t)(i0 + i), buf[i], z);
+            run += w;
         }
-        run += w;
-    }
 }
 
 }  // namespace q8
