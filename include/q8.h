@@ -247,7 +247,7 @@ typedef enum q8_dtype { Q8_F32 = 0, Q8_F16 = 1, Q8_BF16 = 2 } q8_dtype;
  *   not used, whatever they hold; NULL: R for all.  scale: [n_adapters] fp32 or
  *   NULL (1).  adapter: [N] int32.  residual: [N][M] fp32 or NULL (0); it may be
  *   y itself, any other overlap is undefined.  x: [N][K] fp32; y: [N][M] fp32.
- * fp32 sums in a fixed order: |y - exact| <= 2^-24 times (K/256 + 40) times
+ * fp32 sums in a fixed order: |y - exact| <= 2^-24 times (K/128 + 64) times
  *   |scale| sum_j |B_mj| sum_k |A_jk x_k|, plus the roundings of the stored
  *   value; bit-identical from run to run.  An adapter's matrices are read once
  *   for every 4 of its tokens.  One launch.

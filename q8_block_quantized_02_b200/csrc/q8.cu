@@ -922,10 +922,12 @@ static LoraKernel lora_kernel_for(int dtype) {
     return dtype == Q8_F32 ? &lora_kernel<float> : dtype == Q8_F16 ? &lora_kernel<__half> : &lora_kernel<__nv_bfloat16>;
 }
 
-static cudaError_t setup_lora_kernels(int) {
+static cudaError_t setup_lora_kernels(int max_smem) {
     for (int d = 0; d < 3; ++d) {
-        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(lora_kernel_for(d)),
-                                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        const void *k = reinterpret_cast<const void *>(lora_kernel_for(d));
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lora_smem_bytes(kLoraChunk));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -954,13 +956,19 @@ static q8_status lora_check(const LoraArgs &a, int64_t N, int64_t n_adapters, in
     return check_aligned4(a.res, true);
 }
 
-// A cluster per token: 16 CTAs for up to 8 tokens, 8 for more (the clusters
-// then fill the SMs once).
-static q8_status run_lora(const LoraArgs &a, int dtype, cudaStream_t stream) {
+// A cluster per token, of the most CTAs with which the clusters of all tokens
+// run at once.
+static q8_status run_lora(LoraArgs a, int dtype, cudaStream_t stream) {
     const DeviceInfo *dev = nullptr;
     Q8_CHECK(device_info(&dev));
-    const int cl = a.N <= 8 ? 16 : 8;
-    return launch_pdl_cluster(lora_kernel_for(dtype), dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), 0, stream,
+    const LoraKernel kern = lora_kernel_for(dtype);
+    int cl = 16;
+    for (; cl > kLoraMinCluster; --cl)
+        if (a.N * cl <= dev->sms && max_active_clusters(reinterpret_cast<const void *>(kern), kLoraThreads,
+                                                        lora_smem_bytes(kLoraChunk), cl) >= a.N)
+            break;
+    a.chunk = (int)std::min<int64_t>(kLoraChunk, round_up(ceil_div(a.K / 32, cl) * 32, 256));
+    return launch_pdl_cluster(kern, dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), lora_smem_bytes(a.chunk), stream,
                               "q8_lora launch", (unsigned)cl, a);
 }
 
@@ -978,10 +986,14 @@ static q8_status run_gemv_lora(const void *W, const LoraArgs &a, int64_t N, int6
 // sampler
 // ---------------------------------------------------------------------------
 static cudaError_t setup_sample_kernel(int max_smem) {
-    const void *k = reinterpret_cast<const void *>(&sample_kernel);
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const void *ks[2] = {reinterpret_cast<const void *>(&sample_kernel<1>), reinterpret_cast<const void *>(&sample_kernel<2>)};
+    for (const void *k : ks) {
+        cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 static RegisterSetup g_reg_sample(setup_sample_kernel);
 
@@ -1291,7 +1303,7 @@ q8_status q8_moe_route_grouped(const float *logits, const float *bias, int64_t T
 q8_status q8_lora(const float *x, const void *A, const void *B, const int32_t *rank, const float *scale,
                   const int32_t *adapter, const float *residual, float *y, int64_t M, int64_t K, int64_t N,
                   int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream) {
-    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R};
+    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R, 0};
     Q8_CHECK(lora_check(a, N, n_adapters, R, dtype));
     return run_lora(a, dtype, (cudaStream_t)stream);
 }
@@ -1299,14 +1311,14 @@ q8_status q8_lora(const float *x, const void *A, const void *B, const int32_t *r
 q8_status q8_gemv_lora(const void *W, const float *x, const void *A, const void *B, const int32_t *rank,
                        const float *scale, const int32_t *adapter, const float *residual, float *y, int64_t M,
                        int64_t K, int64_t N, int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream) {
-    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R};
+    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R, 0};
     return run_gemv_lora(W, a, N, n_adapters, R, dtype, (cudaStream_t)stream, false);
 }
 
 q8_status q8_gemv_lora_split(const void *W, const float *x, const void *A, const void *B, const int32_t *rank,
                              const float *scale, const int32_t *adapter, const float *residual, float *y, int64_t M,
                              int64_t K, int64_t N, int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream) {
-    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R};
+    const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R, 0};
     return run_gemv_lora(W, a, N, n_adapters, R, dtype, (cudaStream_t)stream, true);
 }
 
@@ -1326,12 +1338,6 @@ q8_status q8_sample(const float *logits, const float *temperature, const int32_t
     Q8_CHECK(check_aligned4(prob, true));
     const DeviceInfo *dev = nullptr;
     Q8_CHECK(device_info(&dev));
-    // A cluster per row, as many CTAs as the row needs to fit in their shared
-    // memory; more while the rows leave SMs free and a CTA keeps 1024 logits.
-    int cl = 1;
-    while (cl < kSampleMaxCluster && (ceil_div(V, cl) > kSampleMaxSlice ||
-                                      (N * cl * 2 <= dev->sms && ceil_div(V, cl * 2) >= 1024)))
-        cl *= 2;
     SampleArgs a{};
     a.logits = logits;
     a.temperature = temperature;
@@ -1343,13 +1349,24 @@ q8_status q8_sample(const float *logits, const float *temperature, const int32_t
     a.prob = prob;
     a.ld = ld;
     a.V = (int)V;
+    // A cluster per row.  The most CTAs (an SM's each, of at least 1024 logits)
+    // with which all rows run at once; when there are more rows than that, the
+    // fewest that hold a row two to an SM (or, V being too large for that, 16).
+    const size_t spread = (size_t)dev->max_smem_optin / 2 + 1024;  // more than half an SM's shared memory
+    const void *one = reinterpret_cast<const void *>(&sample_kernel<1>);
+    int cl = (int)std::min<int64_t>(kSampleMaxCluster, std::max<int64_t>(1, V / 1024));
+    for (; cl > 0; --cl)
+        if (N * cl <= dev->sms && ceil_div(V, cl) <= kSampleMaxSlice &&
+            max_active_clusters(one, kSampleThreads, spread, cl) >= N)
+            break;
+    const bool all_at_once = cl > 0;
+    if (!all_at_once) cl = (int)std::min<int64_t>(kSampleMaxCluster, ceil_div(V, kSampleHalfSlice));
     a.slice = (int)round_up(ceil_div(V, cl), 4);
-    // two CTAs fit on an SM; when the rows do not need that, ask for more than
-    // half an SM's shared memory so that each CTA gets an SM of its own
     size_t smem = sample_smem_bytes(a.slice, cl);
-    if (N * cl <= dev->sms) smem = std::max(smem, (size_t)dev->max_smem_optin / 2 + 1024);
+    if (all_at_once) smem = std::max(smem, spread);
     if (smem > (size_t)dev->max_smem_optin) return Q8_ERR_UNSUPPORTED;
-    return launch_pdl_cluster(sample_kernel, dim3((unsigned)(N * cl)), dim3(kSampleThreads), smem,
+    return launch_pdl_cluster(all_at_once ? &sample_kernel<1> : &sample_kernel<2>, dim3((unsigned)(N * cl)),
+                              dim3(kSampleThreads), smem,
                               (cudaStream_t)stream, "q8_sample launch", (unsigned)cl, a);
 }
 

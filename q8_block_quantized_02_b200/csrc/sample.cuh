@@ -45,6 +45,7 @@ constexpr int kSampleWindow = 2048;  // top-p's window
 constexpr int kSampleShortK = 256;   // largest top_k of the short path
 constexpr int kSampleMaxCluster = 16;
 constexpr int kSampleMaxSlice = 32768;  // logits per CTA
+constexpr int kSampleHalfSlice = 19008; // ... that leave room for two CTAs on an SM
 constexpr double kSampleLive = 30.498476203173505;  // 44 ln 2: smaller weights are zero
 
 typedef unsigned long long u64;
@@ -358,9 +359,9 @@ __device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 b
     return sh.count != 0;
 }
 
-// Histogram of the elements K in [lo, hi] (shift < 0: by the logit's bin, else
-// by digits of K), counts and with MASS masses.  Whole CTA.
-template <bool MASS>
+// Histogram of the elements K in [lo, hi] (FIRST: by the logit's bin, else by
+// digits of K), counts and with MASS masses.  Whole CTA.
+template <bool MASS, bool FIRST>
 __device__ __forceinline__ void sample_histogram(const SampleRow &s, u64 lo, u64 hi, int shift) {
     SampleShared &sh = *s.sh;
     for (int i = s.tid; i < kSampleBins; i += kSampleThreads) {
@@ -368,18 +369,15 @@ __device__ __forceinline__ void sample_histogram(const SampleRow &s, u64 lo, u64
         if (MASS) sh.mass[i] = 0;
     }
     __syncthreads();
-    const uint32_t klo = (uint32_t)(lo >> 32);
+    // (straight-line per element, so that several are in flight)
 #pragma unroll 8
     for (int i = s.tid; i < s.n; i += kSampleThreads) {
         const float l = s.l[i];
-        if (logit_key(l) >= klo) {
-            const u64 k = s.composite(i);
-            if (k >= lo && k <= hi) {
-                const int b = shift < 0 ? s.bin(l) : (int)((hi - k) >> shift);
-                atomicAdd(&sh.cnt[b], 1u);
-                if (MASS) add_mass(&sh.mass[b], s.weight(l));
-            }
-        }
+        const u64 k = s.composite(i);
+        const int b = FIRST ? s.bin(l) : (int)((hi - k) >> shift) & (kSampleBins - 1);
+        const bool in = k >= lo && k <= hi;
+        if (in) atomicAdd(&sh.cnt[b], 1u);
+        if (MASS && in) add_mass(&sh.mass[b], s.weight(l));
     }
     __syncthreads();
 }
@@ -450,9 +448,12 @@ __device__ bool sample_filter(const SampleRow &s, u64 lo, u64 hi, u64 target, do
     u64 before = 0;
     for (int it = 0;; ++it) {
         const int bits = 64 - __clzll((long long)(hi - lo));
-        const int shift = it == 0 ? -1 : max(0, bits - 11);  // later rounds: digits of the composite key
-        if (it > 0 || MASS) cluster_sync_all();              // the last histogram and its sums are no longer read
-        sample_histogram<MASS>(s, lo, hi, shift);
+        const int shift = max(0, bits - 11);     // later rounds: digits of the composite key
+        if (it > 0 || MASS) cluster_sync_all();  // the last histogram and its sums are no longer read
+        if (it == 0)
+            sample_histogram<MASS, true>(s, lo, hi, 0);
+        else
+            sample_histogram<MASS, false>(s, lo, hi, shift);
         if (s.tid == 0) sh.sent = 0;
         sample_share<MASS>(s, 0.f);
         if (s.warp == 0) {  // the crossing group, then its bins from all CTAs
@@ -591,7 +592,10 @@ __device__ __forceinline__ u64 sample_scan(const SampleRow &s, u64 v, u64 *all) 
     return b4 + inc;
 }
 
-__global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleArgs a) {
+// PER_SM: CTAs an SM is to hold (registers for one leave room for more
+// elements in flight).
+template <int PER_SM>
+__global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) uint8_t sample_smem[];
     SampleRow s;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(s.CL));
@@ -790,7 +794,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
         // and a cut below that takes the exact histogram
         s.bin.scale = (float)(128.0 / t64);
         constexpr float kEst = 1.4426950408889634f / 128.f;
-        sample_histogram<false>(s, kt, best, -1);
+        sample_histogram<false, true>(s, kt, best, 0);
         if (tid == 0) sh.sent = 0;
         sample_share<false>(s, kEst);
         if (warp == 0) {
@@ -847,25 +851,34 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
     }
     auto masses = [&](u64 thr, bool window) {
         u64 ma = 0, mb = 0, mk = 0;
-        const uint32_t klo = (uint32_t)((window ? kt : thr) >> 32);
         const uint32_t base = sh.base;
-#pragma unroll 4
-        for (int i = s0 + lane; i < s1; i += 32) {
-            const float l = buf[i];
-            if (logit_key(l) < klo) continue;
-            const u64 k = s.composite(i);
-            const u64 w = s.weight(l);
-            if (k >= thr) mk += w;
-            if (window && k >= kt) {
-                const int b = s.bin(l);
-                if (b < w0)
-                    ma += w;
-                else if (b > w1)
-                    mb += w;
-                else {
-                    const uint32_t at = base + atomicAdd(&sh.sent, 1u);
-                    if (at < kSampleWindow)
-                        for (uint32_t p = 0; p < CL; ++p) st_cluster_u64(map_to_rank(smem_u32(&sh.mass[at]), p), k);
+        auto send = [&](uint32_t at, u64 e) {
+            if (at < kSampleWindow)
+                for (uint32_t p = 0; p < CL; ++p) st_cluster_u64(map_to_rank(smem_u32(&sh.mass[at]), p), e);
+        };
+        constexpr int kStep = 4;  // elements in flight
+        for (int i = s0 + lane; i < s1; i += 32 * kStep) {
+            u64 w[kStep], k[kStep];
+            int b[kStep];
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) {
+                const float l = buf[min(i + 32 * j, s1 - 1)];
+                k[j] = i + 32 * j < s1 ? ((u64)logit_key(l) << 32) | (0xffffffffu - (uint32_t)(i0 + i + 32 * j)) : 0;
+                w[j] = s.weight(l);
+                b[j] = s.bin(l);
+            }
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) {
+                mk += k[j] >= thr ? w[j] : 0;
+                if (window) {
+                    const bool live = k[j] >= kt;
+                    ma += live && b[j] < w0 ? w[j] : 0;
+                    mb += live && b[j] > w1 ? w[j] : 0;
+                    if (live && b[j] >= w0 && b[j] <= w1) {
+                        const uint32_t at = atomicAdd(&sh.sent, 1u);
+                        if (at < kSampleList) sh.list[at] = k[j];  // sent below, by all threads
+                        else send(base + at, k[j]);
+                    }
                 }
             }
         }
@@ -881,6 +894,8 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(const SampleA
             sh.wbelow[warp] = mb;
         }
         __syncthreads();
+        if (window)
+            for (int i = tid; i < (int)min(sh.sent, (uint32_t)kSampleList); i += kSampleThreads) send(base + i, sh.list[i]);
         if (tid < (int)CL) {
             mk = ma = mb = 0;
 #pragma unroll

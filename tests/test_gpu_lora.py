@@ -40,8 +40,10 @@ def bank_of(seed, n, R, M, K, dtype):
 
 
 def bound(mag, y, K, roundings=1):
-    """The header's fp32 bound on the adapters' part, plus a rounding of the stored value each time it is stored."""
-    return (K / 256 + 64) * H24 * mag + roundings * 1.01 * H24 * np.abs(y)
+    """The header's fp32 bound on the adapters' part, plus a rounding of the stored value each time it is stored.
+    K / 128: a lane's chain of fused multiply-adds, K split over 32 lanes and at least 4 CTAs; the rest: warp, warps' and
+    CTAs' sums of u, the scale, 8 products and 4 steps of a row of B."""
+    return (K / 128 + 64) * H24 * mag + roundings * 1.01 * H24 * np.abs(y)
 
 
 def run(x, A, B, rank, scale, adapter, residual, M, K, dtype, R=None, base=None, packed=None, in_place=False, stream=None):
