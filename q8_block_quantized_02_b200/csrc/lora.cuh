@@ -7,13 +7,19 @@
 // once per kLoraTok of its tokens, and the clusters of the others leave.  The
 // cluster's CTAs split K for u, exchange the partial u over distributed shared
 // memory (added in rank order) and split M for B u.  Sums are fp32 in a fixed
-// order.  What it reads is all it costs, so both halves keep many 16-byte loads
-// in flight: a warp takes several rows of A at a time and loads the next
-// columns while it multiplies the last; the first rows of B are on their way
-// before u is exchanged.
+// order.
+//
+// What it reads is all it costs.  For u a warp takes up to 8 rows of A
+// at a time and loads the next columns into registers while it multiplies the
+// last: 64 KB in flight per SM.  (Rings of asynchronous copies in shared memory
+// in its place, twice as deep, measured slower: what shared memory takes, the
+// L1 cache lacks for loads in flight.)  B is fetched to L2 while u is
+// exchanged.
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "q8q8_mma.cuh"
 #include "q8_device.cuh"
@@ -24,8 +30,8 @@ constexpr int kLoraThreads = 512;
 constexpr int kLoraWarps = kLoraThreads / 32;
 constexpr int kLoraTok = 4;        // tokens a cluster serves
 constexpr int kLoraMaxR = 128;
-constexpr int kLoraChunk = 4096;   // most columns of x staged at a time (a multiple of 256)
-constexpr int kLoraBRows = 8;      // rows of B a thread takes together
+constexpr int kLoraChunk = 3328;   // most columns of x staged at a time (a multiple of 256)
+constexpr int kLoraBlock = 64;     // rows of y a warp gathers before it writes them
 constexpr int kLoraMaxN = 16;
 constexpr int kLoraMinCluster = 4;  // the error bound's K / 128 rests on it
 
@@ -43,65 +49,101 @@ struct LoraArgs {
     int chunk;  // columns of x staged at a time: a multiple of 256, at most kLoraChunk
 };
 
-// 8 consecutive elements of an adapter row as fp32.
+// 16 bytes that are read once: not kept in the L1 cache.
+__device__ __forceinline__ ulonglong2 lora_ldg(const ulonglong2 *p) {
+    ulonglong2 v;
+    asm("ld.global.nc.L1::no_allocate.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "l"(p));
+    return v;
+}
+
+// 8 consecutive elements of an adapter row; get(): as four fp32 pairs.
+// keep(): sets the elements from the n-th on to zero, whatever they hold.
 template <typename T>
 struct Lora8;
 template <>
 struct Lora8<float> {
-    float4 a, b;
+    ulonglong2 a, b;
     __device__ __forceinline__ void load(const float *p) {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        a = lora_ldg(reinterpret_cast<const ulonglong2 *>(p));
+        b = lora_ldg(reinterpret_cast<const ulonglong2 *>(p) + 1);
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    __device__ __forceinline__ void from(const void *shared) {
+        a = reinterpret_cast<const ulonglong2 *>(shared)[0];
+        b = reinterpret_cast<const ulonglong2 *>(shared)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_ulonglong2(0, 0); }
+    __device__ __forceinline__ static uint64_t first(uint64_t v, int n) {
+        return n >= 2 ? v : n == 1 ? v & 0xffffffffull : 0;
+    }
+    __device__ __forceinline__ void keep(int n) {
+        a.x = first(a.x, n);
+        a.y = first(a.y, n - 2);
+        b.x = first(b.x, n - 4);
+        b.y = first(b.y, n - 6);
+    }
+    __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
+        v[0] = a.x;
+        v[1] = a.y;
+        v[2] = b.x;
+        v[3] = b.y;
+    }
+};
+struct Lora8Short {  // two-byte elements
+    uint4 q;
+    __device__ __forceinline__ void load(const void *p) {
+        const ulonglong2 v = lora_ldg(static_cast<const ulonglong2 *>(p));
+        q = *reinterpret_cast<const uint4 *>(&v);
+    }
+    __device__ __forceinline__ void from(const void *shared) { q = *static_cast<const uint4 *>(shared); }
+    __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ static uint32_t first(uint32_t v, int n) { return n >= 2 ? v : n == 1 ? v & 0xffffu : 0; }
+    __device__ __forceinline__ void keep(int n) {
+        q.x = first(q.x, n);
+        q.y = first(q.y, n - 2);
+        q.z = first(q.z, n - 4);
+        q.w = first(q.w, n - 6);
     }
 };
 template <>
-struct Lora8<__half> {
-    uint4 q;
-    __device__ __forceinline__ void load(const __half *p) { q = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+struct Lora8<__half> : Lora8Short {
+    __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+            v[i] = pack_u32x2(__float_as_uint(f.x), __float_as_uint(f.y));
         }
     }
 };
 template <>
-struct Lora8<__nv_bfloat16> {
-    uint4 q;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { q = __ldg(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+struct Lora8<__nv_bfloat16> : Lora8Short {
+    __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = pack_u32x2(w[i] << 16, w[i] & 0xffff0000u);
     }
 };
 
-// x of the cluster's tokens, the halves of each 8 columns apart: [token][half][chunk / 8]
-__host__ __device__ inline size_t lora_smem_bytes(int chunk) { return (size_t)kLoraTok * chunk * 4; }
+__device__ __forceinline__ float lora_sum2(uint64_t v) {
+    const float2 f = unpack_f32x2(v);
+    return f.x + f.y;
+}
+
+// Dynamic shared memory: x of a cluster's tokens (at most `tokens`).
+inline size_t lora_smem_bytes(int chunk, int tokens) {
+    return (size_t)(tokens >= 3 ? kLoraTok : tokens) * chunk * 4;
+}
 
 struct LoraShared {
     float part[kLoraMaxR * kLoraTok * 2];  // sums of a task: [rows of its group][tokens]
     float pu[kLoraMaxR * kLoraTok];        // this CTA's share of u, read by the cluster
-    float us[kLoraTok][kLoraMaxR];         // scale u
+    __align__(8) float us[kLoraTok][kLoraMaxR];  // scale u
+    float ys[kLoraWarps][kLoraTok][kLoraBlock];
     int tok[kLoraTok];
 };
 
-// Halves the values that a lane holds at each step (the other half goes to the
-// lane `off` away), so that V values are summed over the lanes with about V
-// shuffles.
+// Halves the n values that a lane holds (the other half goes to the lane `off`
+// away), so that values are summed over lanes with about one shuffle each.
 template <int C>
 __device__ __forceinline__ void lora_fold(float (&v)[C], int lane, int off, int n) {
     const bool up = lane & off;
@@ -114,15 +156,16 @@ __device__ __forceinline__ void lora_fold(float (&v)[C], int lane, int off, int 
     }
 }
 
-// One cluster's work for NT tokens of one adapter.  RB: rows of A a warp takes
-// together.
-template <typename T, int NT, int RB>
-__device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, float4 *xs, uint32_t CL, uint32_t rank,
+// One cluster's work for nt <= NT tokens of one adapter.
+template <typename T, int NT>
+__device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, uint8_t *smem, uint32_t CL, uint32_t rank,
                                              int ad, int nt, int r) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int V = RB * NT;  // values a task sums (a power of two, at most 32)
+    constexpr int ES = sizeof(T);
+    constexpr int RB = (NT == 1 ? 16 : 8) / ES;     // rows of A a warp takes together (what the registers hold)
+    constexpr int V = RB * NT;                      // values a task sums (a power of two, at most 32)
     const int half = a.chunk / 8;
-    auto xat = [&](int t, int h, int u) -> float4 & { return xs[(t * 2 + h) * half + u]; };
+    ulonglong2 *xs = reinterpret_cast<ulonglong2 *>(smem);  // [token][half of 8][chunk / 8]
 
     // u: this CTA's columns [k0, k1)
     const int64_t k_per = ((a.K / 32 + CL - 1) / CL) * 32;
@@ -134,55 +177,64 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
     for (int i = tid; i < tasks * V; i += kLoraThreads) sh.part[i] = 0.f;
     for (int64_t c0 = k0; c0 < k1; c0 += a.chunk) {
         const int units = (int)min((int64_t)a.chunk, k1 - c0) / 8;
-        __syncthreads();
+        // units of 8 columns of the rows of a task's group
+        auto load = [&](Lora8<T>(&w)[RB], int g, int un) {
+            const T *row = A + (int64_t)(g * RB) * a.K + c0 + 8 * un;
+#pragma unroll
+            for (int j = 0; j < RB; ++j) {
+                w[j].zero();
+                if (un < units && g * RB + j < r) w[j].load(row + j * a.K);
+            }
+        };
+        Lora8<T> cur[RB], nxt[RB];
+        int g = warp / ks, u0 = (warp % ks) * 32 + lane;
+        if (warp < tasks) load(cur, g, u0);  // on its way while x is staged
+        __syncthreads();  // (x of the last chunk is no longer read)
         for (int i = tid; i < NT * units * 2; i += kLoraThreads) {
             const int t = i / (units * 2), q = i % (units * 2);
-            xat(t, q & 1, q >> 1) = t < nt ? __ldg(reinterpret_cast<const float4 *>(a.x + sh.tok[t] * a.K + c0) + q)
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            xs[(t * 2 + (q & 1)) * half + (q >> 1)] =
+                t < nt ? __ldg(reinterpret_cast<const ulonglong2 *>(a.x + sh.tok[t] * a.K + c0) + q)
+                       : make_ulonglong2(0, 0);
         }
         __syncthreads();
         for (int task = warp; task < tasks; task += kLoraWarps) {
-            const int g = task / ks, s = task % ks;
-            float acc[V];
+            uint64_t acc2[V];  // even and odd columns
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = 0.f;
-            const T *row[RB];
-#pragma unroll
-            for (int j = 0; j < RB; ++j) row[j] = A + (int64_t)min(g * RB + j, r - 1) * a.K + c0;
-            Lora8<T> cur[RB], nxt[RB];
-            auto load = [&](Lora8<T>(&w)[RB], int un) {
-#pragma unroll
-                for (int j = 0; j < RB; ++j) {
-                    w[j].zero();
-                    if (un < units) w[j].load(row[j] + 8 * un);
-                }
-            };
-            load(cur, s * 32 + lane);
-            for (int un = s * 32 + lane; un - lane < units; un += ks * 32) {
-                load(nxt, un + ks * 32);
+            for (int i = 0; i < V; ++i) acc2[i] = 0;
+            const int next_g = (task + kLoraWarps) / ks, next_u0 = ((task + kLoraWarps) % ks) * 32 + lane;
+            for (int un = u0; un - lane < units; un += ks * 32) {
+                // the next columns, or the next task's first
+                const bool more = un - lane + ks * 32 < units;
+                load(nxt, more ? g : next_g, more ? un + ks * 32 : next_u0);
                 if (un < units) {
+                    ulonglong2 x[NT][2];
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        const float4 p = xat(t, 0, un), q = xat(t, 1, un);
+                        x[t][0] = xs[(t * 2) * half + un];
+                        x[t][1] = xs[(t * 2 + 1) * half + un];
+                    }
 #pragma unroll
-                        for (int j = 0; j < RB; ++j) {
-                            float wf[8];
-                            cur[j].get(wf);
-                            float &v = acc[j * NT + t];
-                            v = fmaf(wf[0], p.x, v);
-                            v = fmaf(wf[1], p.y, v);
-                            v = fmaf(wf[2], p.z, v);
-                            v = fmaf(wf[3], p.w, v);
-                            v = fmaf(wf[4], q.x, v);
-                            v = fmaf(wf[5], q.y, v);
-                            v = fmaf(wf[6], q.z, v);
-                            v = fmaf(wf[7], q.w, v);
+                    for (int j = 0; j < RB; ++j) {
+                        uint64_t w[4];
+                        cur[j].get(w);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            uint64_t &v = acc2[j * NT + t];
+                            v = fma_f32x2(w[0], x[t][0].x, v);
+                            v = fma_f32x2(w[1], x[t][0].y, v);
+                            v = fma_f32x2(w[2], x[t][1].x, v);
+                            v = fma_f32x2(w[3], x[t][1].y, v);
                         }
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < RB; ++j) cur[j] = nxt[j];
             }
+            g = next_g;
+            u0 = next_u0;
+            float acc[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = lora_sum2(acc2[i]);
             int off = 16, n = V;
 #pragma unroll
             for (int st = 0; st < 5; ++st, off >>= 1) {
@@ -193,30 +245,26 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
                     acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], off);
                 }
             }
-            // lane holds the value whose index is its top bits
+            // a lane holds the value whose index is its top bits
             if (lane % (32 / V) == 0) sh.part[task * V + lane / (32 / V)] += acc[0];
         }
     }
 
-    // the first rows of B set out before u is known
-    const int64_t m_per = (((a.M + CL - 1) / CL) + 7) / 8 * 8;
+    // B: the CTA's rows [m0, m1), a contiguous part of them for each warp, sent
+    // for (to L2) while u is exchanged
+    const int64_t m_per = (a.M + CL - 1) / CL;
     const int64_t m0 = min(a.M, m_per * rank), m1 = min(a.M, m0 + m_per);
-    const int bu = (r + 7) / 8;  // 8-column units of a row of B
-    int lanes = 1;               // threads that share a row
-    while (lanes < bu) lanes <<= 1;
-    const int jc = lane & (lanes - 1);
-    const T *B = static_cast<const T *>(a.B) + (int64_t)ad * a.M * a.R + jc * 8;
-    const int64_t step = (int64_t)kLoraThreads / lanes * kLoraBRows;
-    int64_t mb = m0 + (int64_t)(tid / lanes) * kLoraBRows;
-    Lora8<T> w[kLoraBRows];
-    auto load_b = [&](int64_t m) {
-#pragma unroll
-        for (int j = 0; j < kLoraBRows; ++j) {
-            w[j].zero();
-            if (m + j < m1 && jc < bu) w[j].load(B + (m + j) * a.R);
-        }
-    };
-    load_b(mb);
+    const int64_t w_per = (m1 - m0 + kLoraWarps - 1) / kLoraWarps;
+    const int64_t w0 = min(m1, m0 + w_per * warp), w1 = min(m1, w0 + w_per);
+    const T *B = static_cast<const T *>(a.B) + (int64_t)ad * a.M * a.R;
+#pragma unroll 1
+    for (int64_t o = w0 * a.R + lane * (128 / ES); o < w1 * a.R; o += 32 * (128 / ES))
+        if (o % a.R < r) asm volatile("prefetch.global.L2 [%0];" ::"l"(B + o));
+    if (a.res)
+        for (int t = 0; t < nt; ++t)
+#pragma unroll 1
+            for (int64_t m = w0 + lane * 8; m < w1; m += 256)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.res + sh.tok[t] * a.M + m));
 
     __syncthreads();
     for (int i = tid; i < r * NT; i += kLoraThreads) {
@@ -225,8 +273,8 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
         for (int s = 0; s < ks; ++s) v += sh.part[((j / RB) * ks + s) * V + (j % RB) * NT + t];
         sh.pu[i] = v;
     }
-    cluster_sync_all();
     const float sc = a.scale ? __ldg(a.scale + ad) : 1.f;
+    cluster_sync_all();
     for (int i = tid; i < kLoraMaxR * NT; i += kLoraThreads) {
         float v[16];
 #pragma unroll
@@ -236,60 +284,75 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
         for (uint32_t p = 1; p < 16; ++p) v[0] += v[p];
         sh.us[i % NT][i / NT] = sc * v[0];
     }
-    // pu is not read after this barrier completes; it is waited for at the end
+    // pu is not read any more; the barrier is waited for before the CTA ends
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     __syncthreads();
 
-    float uf[NT][8];
+    const int bu = (r + 7) / 8;  // 8-column units of a row of B
+    int lanes = 1;               // lanes that share a row, one unit each
+    while (lanes < bu) lanes <<= 1;
+    const int jc = lane & (lanes - 1), grp = lane / lanes, G = 32 / lanes;
+    const int kept = min(max(r - jc * 8, 0), 8);  // what lies past the rank is not used
+    uint64_t uf[NT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) uf[t][i] = sh.us[t][jc * 8 + i];
-    const int64_t rounds = m1 > m0 ? (m1 - m0 + step - 1) / step : 0;
-    for (int64_t it = 0; it < rounds; ++it, mb += step) {
-        constexpr int VB = kLoraBRows * NT;
-        float v[VB];
+        for (int i = 0; i < 4; ++i) uf[t][i] = *reinterpret_cast<const uint64_t *>(&sh.us[t][jc * 8 + 2 * i]);
+#pragma unroll 1
+    for (int64_t m = w0; m < w1; m += kLoraBlock) {
+        const int rows = (int)min((int64_t)kLoraBlock, w1 - m);
+        float out[2][NT];  // the residuals, all loaded before any is stored over
 #pragma unroll
-        for (int j = 0; j < kLoraBRows; ++j) {
-            float wf[8];
-            w[j].get(wf);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) v[j * NT + t] = 0.f;
+            for (int t = 0; t < NT; ++t)
+                out[h][t] = a.res && t < nt && lane + 32 * h < rows ? a.res[sh.tok[t] * a.M + m + lane + 32 * h] : 0.f;
+        // (kept short: code that runs once is paid for in instruction fetches)
+        constexpr int RT = NT == 4 ? 2 : 4;  // rows a lane takes together
+#pragma unroll 1
+        for (int j = grp; j - grp < rows; j += RT * G) {
+            float v[RT][NT];
+            Lora8<T> q[RT];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float b = jc * 8 + i < r ? wf[i] : 0.f;  // what lies past the rank is not used
-#pragma unroll
-                for (int t = 0; t < NT; ++t) v[j * NT + t] = fmaf(b, uf[t][i], v[j * NT + t]);
+            for (int i = 0; i < RT; ++i) {
+                q[i].zero();
+                if (j + i * G < rows && jc < bu) q[i].load(B + (m + j + i * G) * a.R + jc * 8);
             }
-        }
-        if (it + 1 < rounds) load_b(mb + step);
-        // sum over the row's threads
-        int n = VB, at = 0;
-        bool mine = true;
 #pragma unroll
-        for (int st = 0; st < 4; ++st) {
-            const int off = lanes >> (st + 1);
-            if (off > 0) {
-                if (VB >> st > 1) {
-                    lora_fold<VB>(v, lane, off, VB >> st);
-                    if (lane & off) at += VB >> (st + 1);
-                    n = VB >> (st + 1);
-                } else {
-                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
-                    mine = mine && !(lane & off);
+            for (int i = 0; i < RT; ++i) {
+                if (kept < 8) q[i].keep(kept);
+                uint64_t w[4];
+                q[i].get(w);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    uint64_t s2 = mul_f32x2(w[0], uf[t][0]);
+                    s2 = fma_f32x2(w[1], uf[t][1], s2);
+                    s2 = fma_f32x2(w[2], uf[t][2], s2);
+                    s2 = fma_f32x2(w[3], uf[t][3], s2);
+                    v[i][t] = lora_sum2(s2);
                 }
             }
-        }
+#pragma unroll 1
+            for (int off = lanes >> 1; off > 0; off >>= 1)
 #pragma unroll
-        for (int i = 0; i < VB; ++i)
-            if (i < n && mine) {
-                const int t = (at + i) % NT;
-                const int64_t m = mb + (at + i) / NT;
-                if (t < nt && m < m1) {
-                    const int64_t o = sh.tok[t] * a.M + m;
-                    a.y[o] = (a.res ? a.res[o] : 0.f) + v[i];
-                }
-            }
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) v[i][t] += __shfl_xor_sync(0xffffffffu, v[i][t], off);
+            if (jc == 0)
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    if (j + i * G < rows)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) sh.ys[warp][t][j + i * G] = v[i][t];
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (t < nt && lane + 32 * h < rows)
+                    a.y[sh.tok[t] * a.M + m + lane + 32 * h] = out[h][t] + sh.ys[warp][t][lane + 32 * h];
+        __syncwarp();
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -328,15 +391,12 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs a)
     __syncthreads();
     int r = a.R;
     if (a.rank) r = min(max(__ldg(a.rank + ad), 0), a.R);
-    float4 *xs = reinterpret_cast<float4 *>(lora_smem);
-    // fp32 rows take twice the registers
-    constexpr int RB = sizeof(T) == 4 ? 4 : 8;
     if (nt == 1)
-        lora_cluster<T, 1, RB>(a, sh, xs, CL, rank, ad, nt, r);
+        lora_cluster<T, 1>(a, sh, lora_smem, CL, rank, ad, nt, r);
     else if (nt == 2)
-        lora_cluster<T, 2, RB>(a, sh, xs, CL, rank, ad, nt, r);
+        lora_cluster<T, 2>(a, sh, lora_smem, CL, rank, ad, nt, r);
     else
-        lora_cluster<T, 4, 4>(a, sh, xs, CL, rank, ad, nt, r);
+        lora_cluster<T, 4>(a, sh, lora_smem, CL, rank, ad, nt, r);
 }
 
 }  // namespace q8

@@ -927,7 +927,8 @@ static cudaError_t setup_lora_kernels(int max_smem) {
         const void *k = reinterpret_cast<const void *>(lora_kernel_for(d));
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)lora_smem_bytes(kLoraChunk));
+        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)lora_smem_bytes(kLoraChunk, kLoraTok));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -956,19 +957,32 @@ static q8_status lora_check(const LoraArgs &a, int64_t N, int64_t n_adapters, in
     return check_aligned4(a.res, true);
 }
 
+// The largest cluster, of at most `most` CTAs, of which `n` run at once (one CTA
+// per SM), or `least`.  Found once per device, kernel (`slot`) and n; n <= 160.
+static int cluster_for(int slot, int64_t n, const void *kernel, int threads, size_t smem, int sms, int most, int least) {
+    static std::atomic<signed char> known[kMaxDevices][4][161];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || n > 160) return least;
+    std::atomic<signed char> &k = known[dev][slot][n];
+    int cl = k.load(std::memory_order_relaxed);
+    if (cl == 0) {
+        for (cl = 16; cl > 1; --cl)
+            if (n * cl <= sms && max_active_clusters(kernel, threads, smem, cl) >= n) break;
+        k.store((signed char)cl, std::memory_order_relaxed);
+    }
+    return std::max(least, std::min(cl, most));
+}
+
 // A cluster per token, of the most CTAs with which the clusters of all tokens
 // run at once.
 static q8_status run_lora(LoraArgs a, int dtype, cudaStream_t stream) {
     const DeviceInfo *dev = nullptr;
     Q8_CHECK(device_info(&dev));
     const LoraKernel kern = lora_kernel_for(dtype);
-    int cl = 16;
-    for (; cl > kLoraMinCluster; --cl)
-        if (a.N * cl <= dev->sms && max_active_clusters(reinterpret_cast<const void *>(kern), kLoraThreads,
-                                                        lora_smem_bytes(kLoraChunk), cl) >= a.N)
-            break;
+    const int cl = cluster_for(dtype, a.N, reinterpret_cast<const void *>(kern), kLoraThreads,
+                               lora_smem_bytes(kLoraChunk, kLoraTok), dev->sms, 16, kLoraMinCluster);
     a.chunk = (int)std::min<int64_t>(kLoraChunk, round_up(ceil_div(a.K / 32, cl) * 32, 256));
-    return launch_pdl_cluster(kern, dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), lora_smem_bytes(a.chunk), stream,
+    return launch_pdl_cluster(kern, dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), lora_smem_bytes(a.chunk, a.N), stream,
                               "q8_lora launch", (unsigned)cl, a);
 }
 
@@ -1353,13 +1367,9 @@ q8_status q8_sample(const float *logits, const float *temperature, const int32_t
     // with which all rows run at once; when there are more rows than that, the
     // fewest that hold a row two to an SM (or, V being too large for that, 16).
     const size_t spread = (size_t)dev->max_smem_optin / 2 + 1024;  // more than half an SM's shared memory
-    const void *one = reinterpret_cast<const void *>(&sample_kernel<1>);
-    int cl = (int)std::min<int64_t>(kSampleMaxCluster, std::max<int64_t>(1, V / 1024));
-    for (; cl > 0; --cl)
-        if (N * cl <= dev->sms && ceil_div(V, cl) <= kSampleMaxSlice &&
-            max_active_clusters(one, kSampleThreads, spread, cl) >= N)
-            break;
-    const bool all_at_once = cl > 0;
+    int cl = cluster_for(3, N, reinterpret_cast<const void *>(&sample_kernel<1>), kSampleThreads, spread, dev->sms,
+                         (int)std::max<int64_t>(1, V / 1024), 1);
+    const bool all_at_once = N * cl <= dev->sms && ceil_div(V, cl) <= kSampleMaxSlice;
     if (!all_at_once) cl = (int)std::min<int64_t>(kSampleMaxCluster, ceil_div(V, kSampleHalfSlice));
     a.slice = (int)round_up(ceil_div(V, cl), 4);
     size_t smem = sample_smem_bytes(a.slice, cl);
