@@ -68,7 +68,7 @@ struct alignas(16) SampleInbox {
     u64 gmass[kSampleGroups];      // a group's mass, or the bits of its fp32 estimate
     uint32_t gcnt[kSampleGroups];
     u64 best;                      // largest composite key
-    u64 above, below, kept;        // masses of the pass over the weights
+    u64 above, all, kept;          // masses of the pass over the weights
     uint32_t sent;                 // elements of the short list
 };
 
@@ -81,7 +81,7 @@ struct alignas(16) SampleShared {
     u64 list[kSampleList];
     uint32_t cnt[kSampleBins];  // read by the cluster
     double tab[256];            // 2^(-j / 256)
-    u64 wsum[kSampleWarps], wabove[kSampleWarps], wbelow[kSampleWarps];
+    u64 wsum[kSampleWarps], wabove[kSampleWarps], wall[kSampleWarps];
     u64 gm[32];                 // group sums of a list's histogram
     u64 tiny[32];
     uint32_t tiny_n;
@@ -208,6 +208,10 @@ struct SampleRow {
     int tid, warp, lane;
     SampleWeight weight;
     SampleBinning bin;
+    // Whether element i's composite key is at least K, l being its logit (above -inf).
+    __device__ __forceinline__ bool at_least(float l, int i, float K_logit, uint32_t K_low) const {
+        return l > K_logit || (l == K_logit && 0xffffffffu - (uint32_t)(i0 + i) >= K_low);
+    }
     __device__ __forceinline__ u64 composite(int i) const {
         return ((u64)logit_key(l[i]) << 32) | (0xffffffffu - (uint32_t)(i0 + i));
     }
@@ -223,24 +227,16 @@ __device__ __forceinline__ void add_mass(u64 *at, u64 w) {
 }
 
 // The list entry at which, in descending order, the running count (MASS: mass)
-// from `before` reaches `target`; with MASS and target 0 the target is top_p of
-// `other` and the list's mass together.  False when that does not lie in the
-// list.  Whole CTA.
+// from `before` reaches `target`.  False when that does not lie in the list.
+// Whole CTA.
 template <bool MASS>
-__device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 before, u64 target, double top_p, u64 other,
-                                   u64 *kt) {
+__device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 before, u64 target, u64 *kt) {
     SampleShared &sh = *s.sh;
     const u64 *list = window ? sh.mass : sh.list;
     u64 *mass = window ? sh.list : sh.mass;  // 1024 bins
     uint32_t count = (uint32_t)n;
     u64 lo = 0, hi = ~0ull;
     bool first = true;
-    auto settle_target = [&](u64 all) {
-        if (MASS && target == 0) {
-            target = (u64)ceil(top_p * (double)(other + all));
-            if (target < 1) target = 1;
-        }
-    };
     if (count > 32) {
         u64 mn = ~0ull, mxv = 0;
         for (int i = s.tid; i < n; i += kSampleThreads) {
@@ -301,7 +297,6 @@ __device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 b
         if (s.warp == 0) {
             u64 v = sh.gm[s.lane];
             u64 inc = before + warp_incl_scan(v, s.lane);
-            if (first) settle_target(__shfl_sync(0xffffffffu, inc, 31) - before);
             const unsigned cross = __ballot_sync(0xffffffffu, inc - v < target && target <= inc);
             if (cross) {
                 const int g = __ffs(cross) - 1;
@@ -316,7 +311,6 @@ __device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 b
                     sh.lo = top - lo > span ? top - span : lo;
                     sh.before = inc - v;
                     sh.count = c;
-                    sh.target = target;
                 }
             } else if (s.lane == 0) {
                 sh.count = 0;
@@ -326,7 +320,6 @@ __device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 b
         lo = sh.lo;
         hi = sh.hi;
         before = sh.before;
-        target = sh.target;
         count = sh.count;
         first = false;
         __syncthreads();
@@ -343,7 +336,6 @@ __device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 b
         const int tn = min((int)sh.tiny_n, 32);
         const u64 e = s.lane < tn ? sh.tiny[s.lane] : 0;
         const u64 w = s.lane >= tn ? 0 : MASS ? s.weight(key_logit((uint32_t)(e >> 32))) : 1;
-        if (first) settle_target(warp_sum(w));
         u64 ex = before;
         for (int j = 0; j < tn; ++j) {
             const u64 ej = __shfl_sync(0xffffffffu, e, j), wj = __shfl_sync(0xffffffffu, w, j);
@@ -369,15 +361,29 @@ __device__ __forceinline__ void sample_histogram(const SampleRow &s, u64 lo, u64
         if (MASS) sh.mass[i] = 0;
     }
     __syncthreads();
-    // (straight-line per element, so that several are in flight)
-#pragma unroll 8
-    for (int i = s.tid; i < s.n; i += kSampleThreads) {
-        const float l = s.l[i];
-        const u64 k = s.composite(i);
-        const int b = FIRST ? s.bin(l) : (int)((hi - k) >> shift) & (kSampleBins - 1);
-        const bool in = k >= lo && k <= hi;
-        if (in) atomicAdd(&sh.cnt[b], 1u);
-        if (MASS && in) add_mass(&sh.mass[b], s.weight(l));
+    if (FIRST) {  // (hi is the row's largest)
+        const float lo_l = key_logit((uint32_t)(lo >> 32));
+        const uint32_t lo_w = (uint32_t)lo;
+#pragma unroll 2
+        for (int j = s.tid; 4 * j < s.n; j += kSampleThreads) {
+            const float4 q = reinterpret_cast<const float4 *>(s.l)[j];
+            const float l[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bool in = s.at_least(l[c], 4 * j + c, lo_l, lo_w);
+                if (in) atomicAdd(&sh.cnt[s.bin(l[c])], 1u);
+                if (MASS && in) add_mass(&sh.mass[s.bin(l[c])], s.weight(l[c]));
+            }
+        }
+    } else {
+        for (int i = s.tid; i < s.n; i += kSampleThreads) {
+            const u64 k = s.composite(i);
+            if (k >= lo && k <= hi) {
+                const int b = (int)((hi - k) >> shift);
+                atomicAdd(&sh.cnt[b], 1u);
+                if (MASS) add_mass(&sh.mass[b], s.weight(s.l[i]));
+            }
+        }
     }
     __syncthreads();
 }
@@ -544,7 +550,7 @@ __device__ bool sample_filter(const SampleRow &s, u64 lo, u64 hi, u64 target, do
                 }
             }
             cluster_sync_all();
-            sample_list_select<MASS>(s, false, (int)bc, before, target, 0.0, 0, kt);
+            sample_list_select<MASS>(s, false, (int)bc, before, target, kt);
             return true;
         }
         lo = nlo;
@@ -644,6 +650,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
 #pragma unroll 8
             for (int i = tid; i < n; i += kSampleThreads) buf[i] = take(__ldg(src + i), i);
         }
+        if (tid < (-n & 3)) buf[n + tid] = -INFINITY;  // the last four are read together
         if (mi != 0x7fffffff) best = ((u64)logit_key(mv) << 32) | (0xffffffffu - (uint32_t)(i0 + mi));
     }
     const u64 own = best;  // this thread's largest
@@ -731,14 +738,17 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
             __syncthreads();
             // the elements down to that bin: gathered here, then sent to rank 0
             const int b = sh.bin;
-            const uint32_t klo = (uint32_t)(kt >> 32);
-#pragma unroll 8
-            for (int i = tid; i < n; i += kSampleThreads) {
-                const float l = buf[i];
-                if (s.bin(l) <= b && logit_key(l) >= klo) {
-                    const uint32_t at = atomicAdd(&sh.sent, 1u);
-                    if (at < kSampleThreads) sh.mass[at] = s.composite(i);
-                }
+            const float live = key_logit((uint32_t)(kt >> 32));
+#pragma unroll 4
+            for (int j = tid; 4 * j < n; j += kSampleThreads) {
+                const float4 q = reinterpret_cast<const float4 *>(buf)[j];
+                const float l[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (s.bin(l[c]) <= b && l[c] >= live) {
+                        const uint32_t at = atomicAdd(&sh.sent, 1u);
+                        if (at < kSampleThreads) sh.mass[at] = s.composite(4 * j + c);
+                    }
             }
             __syncthreads();
             const uint32_t sent = sh.sent;
@@ -849,65 +859,68 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
         n_list = sh.above;
         if (n_list > kSampleWindow) w1 = -1;  // no list: the exact histogram
     }
+    // Sums of the CTA's weights K >= thr (kept); with a window also of all and
+    // of those above it, its elements going to the list.
     auto masses = [&](u64 thr, bool window) {
-        u64 ma = 0, mb = 0, mk = 0;
+        u64 ma = 0, mt = 0, mk = 0;
         const uint32_t base = sh.base;
         auto send = [&](uint32_t at, u64 e) {
             if (at < kSampleWindow)
                 for (uint32_t p = 0; p < CL; ++p) st_cluster_u64(map_to_rank(smem_u32(&sh.mass[at]), p), e);
         };
-        constexpr int kStep = 4;  // elements in flight
-        for (int i = s0 + lane; i < s1; i += 32 * kStep) {
-            u64 w[kStep], k[kStep];
-            int b[kStep];
+        const float thr_l = key_logit((uint32_t)(thr >> 32)), kt_l = key_logit((uint32_t)(kt >> 32));
+        const uint32_t thr_w = (uint32_t)thr, kt_w = (uint32_t)kt;
+        const bool kept = !window || thr > kt;  // else it comes out of the other sums
+#pragma unroll 1
+        for (int i = s0 + 4 * lane; i < s1; i += 128) {  // four elements in flight
+            const float4 q = *reinterpret_cast<const float4 *>(buf + i);
+            const float l[4] = {q.x, q.y, q.z, q.w};
+            u64 w[4];
 #pragma unroll
-            for (int j = 0; j < kStep; ++j) {
-                const float l = buf[min(i + 32 * j, s1 - 1)];
-                k[j] = i + 32 * j < s1 ? ((u64)logit_key(l) << 32) | (0xffffffffu - (uint32_t)(i0 + i + 32 * j)) : 0;
-                w[j] = s.weight(l);
-                b[j] = s.bin(l);
-            }
+            for (int c = 0; c < 4; ++c) w[c] = s.weight(l[c]);
+            if (kept)
 #pragma unroll
-            for (int j = 0; j < kStep; ++j) {
-                mk += k[j] >= thr ? w[j] : 0;
-                if (window) {
-                    const bool live = k[j] >= kt;
-                    ma += live && b[j] < w0 ? w[j] : 0;
-                    mb += live && b[j] > w1 ? w[j] : 0;
-                    if (live && b[j] >= w0 && b[j] <= w1) {
+                for (int c = 0; c < 4; ++c) mk += s.at_least(l[c], i + c, thr_l, thr_w) ? w[c] : 0;
+            if (window)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const bool live = s.at_least(l[c], i + c, kt_l, kt_w);
+                    const int b = s.bin(l[c]);
+                    mt += live ? w[c] : 0;
+                    ma += live && b < w0 ? w[c] : 0;
+                    if (live && b >= w0 && b <= w1) {
                         const uint32_t at = atomicAdd(&sh.sent, 1u);
-                        if (at < kSampleList) sh.list[at] = k[j];  // sent below, by all threads
-                        else send(base + at, k[j]);
+                        if (at < kSampleList) sh.list[at] = s.composite(i + c);  // sent below, by all threads
+                        else send(base + at, s.composite(i + c));
                     }
                 }
-            }
         }
         mk = warp_sum(mk);
         if (window) {
             ma = warp_sum(ma);
-            mb = warp_sum(mb);
+            mt = warp_sum(mt);
         }
         __syncthreads();
         if (lane == 0) {
             sh.wsum[warp] = mk;
             sh.wabove[warp] = ma;
-            sh.wbelow[warp] = mb;
+            sh.wall[warp] = mt;
         }
         __syncthreads();
         if (window)
             for (int i = tid; i < (int)min(sh.sent, (uint32_t)kSampleList); i += kSampleThreads) send(base + i, sh.list[i]);
         if (tid < (int)CL) {
-            mk = ma = mb = 0;
+            mk = ma = mt = 0;
 #pragma unroll
             for (int w = 0; w < kSampleWarps; ++w) {
                 mk += sh.wsum[w];
                 ma += sh.wabove[w];
-                mb += sh.wbelow[w];
+                mt += sh.wall[w];
             }
             const uint32_t box = smem_u32(&s.inbox[rank]);
             st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, kept), tid), mk);
             st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, above), tid), ma);
-            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, below), tid), mb);
+            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, all), tid), mt);
         }
         cluster_sync_all();
     };
@@ -923,10 +936,11 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
             for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
                 if (p < CL) {
                     above += s.inbox[p].above;
-                    z += s.inbox[p].below;
+                    z += s.inbox[p].all;
                 }
-            u64 cut;
-            found = sample_list_select<true>(s, true, (int)n_list, above, 0, (double)top_p, above + z, &cut);
+            u64 target = (u64)ceil((double)top_p * (double)z), cut;
+            if (target < 1) target = 1;
+            found = above < target && sample_list_select<true>(s, true, (int)n_list, above, target, &cut);
             if (found) kt = cut;
         }
         if (!found) {
