@@ -215,6 +215,30 @@ def test_captured_replays_follow_new_inputs_on_another_stream():
     assert q8().q8_read_device_error() == (0, 0)
 
 
+def test_long_reductions_and_many_rows():
+    """K beyond what a cluster stages of x at once, and M beyond what its warps gather at once."""
+    for M, K, R, dtype in ((5, 70016, 16, "bf16"), (40007, 96, 8, "f16"), (20011, 128, 128, "f32")):
+        A, B, scale, An, Bn = bank_of(M, 2, R, M, K, dtype)
+        g = np.random.default_rng(K)
+        x = g.standard_normal((5, K)).astype(np.float32)
+        res = g.standard_normal((5, M)).astype(np.float32)
+        adapter = [0, 1, 0, 0, -1]
+        y_ref, mag = refs.lora(x, An, Bn, [R, R - 3], scale, adapter, res)
+        y = run(x, A.cuda(), B.cuda(), [R, R - 3], scale, adapter, res, M, K, dtype, in_place=M > 1000)
+        assert_within(y, y_ref, bound(mag, y_ref, K), f"{M}x{K} R={R}")
+
+
+def test_nan_and_infinite_activations_stay_in_their_row():
+    M, K, R = 100, 256, 16
+    A, B, scale, An, Bn = bank_of(40, 2, R, M, K, "bf16")
+    x = np.random.default_rng(41).standard_normal((5, K)).astype(np.float32)
+    x[1, 7], x[3, 9] = np.nan, np.inf
+    y = run(x, A.cuda(), B.cuda(), None, scale, [0, 0, 0, 0, 1], None, M, K, "bf16")
+    assert np.all(np.isnan(y[1])) and not np.any(np.isfinite(y[3]))
+    y_ref, mag = refs.lora(x[[0, 2, 4]], An, Bn, None, scale, [0, 0, 1], None)
+    assert_within(y[[0, 2, 4]], y_ref, bound(mag, y_ref, K), "the other rows")
+
+
 def test_misaligned_and_host_pointers_are_refused():
     t = torch()
     M, K, R = 16, 64, 8

@@ -112,6 +112,43 @@ def test_threshold_around_zero_logits():
     check(l, top_k=np.array(mid) + 20, u=g.random(6).astype(np.float32))
 
 
+@pytest.mark.parametrize("kw", [dict(top_k=200), dict(top_k=256, top_p=0.6), dict(top_k=257), dict(top_k=200, min_p=0.5)])
+def test_large_logits_crowded_in_one_place(kw):
+    """The largest logits side by side (few threads hold them), or at a stride (one thread holds most of them)."""
+    g = np.random.default_rng(13)
+    V = 100000
+    l = g.standard_normal((4, V)).astype(np.float32)
+    l[0, 500:3500] = 8 + np.arange(3000, dtype=np.float32) * 1e-3
+    l[1, 90000:90600] = 9 - np.arange(600, dtype=np.float32) * 1e-4
+    l[2, ::2048] = 7 + g.random(l[2, ::2048].size).astype(np.float32)
+    l[3, 3::512] = 7.0
+    check(l, u=g.random(4).astype(np.float32), **kw)
+
+
+@pytest.mark.parametrize("top_p", [0.2, 0.5, 0.8, 0.97, 0.9995])
+def test_mass_in_few_tokens(top_p):
+    """Peaked rows, where the estimate of top-p's bin is at its coarsest: one, two, ten and a hundred heavy tokens."""
+    g = np.random.default_rng(14)
+    l = g.standard_normal((8, 60000)).astype(np.float32)
+    for n, heavy in enumerate((1, 2, 2, 10, 10, 100, 100, 1000)):
+        l[n, g.choice(60000, heavy, replace=False)] = 14 + (n % 2) * g.random(heavy).astype(np.float32) * 3
+    check(l, top_p=top_p, u=g.random(8).astype(np.float32))
+    check(l, top_p=top_p, temperature=2.5, min_p=0.01, u=g.random(8).astype(np.float32))
+
+
+@pytest.mark.parametrize("V", [1024, 1025, 19008, 19009, 32768, 32769])
+@pytest.mark.parametrize("N", [1, 20, 75, 149, 161])
+def test_cluster_sizes(V, N):
+    """Around the sizes and batches at which a row takes another number of CTAs."""
+    g = np.random.default_rng(V + N)
+    l = np.repeat((g.standard_normal((1, V)) * 1.5).astype(np.float32), N, 0)
+    u = g.random(N).astype(np.float32)
+    token, prob = sample(l, top_p=0.9, u=u)
+    for n in sorted({0, N // 2, N - 1}):
+        rt, rp, _ = refs.sample_row(l[0], top_p=np.float32(0.9), u=u[n])
+        assert token[n] == rt and abs(prob[n] - rp) <= (2.0 ** -24 * 1.0001 + V * 2.0 ** -44) * rp
+
+
 def test_masks_infinities_and_nan():
     g = np.random.default_rng(7)
     V = 5003
