@@ -80,7 +80,7 @@ struct alignas(16) SampleShared {
     u64 mass[kSampleBins];
     u64 list[kSampleList];
     uint32_t cnt[kSampleBins];  // read by the cluster
-    double tab[256];            // 2^(-j / 256)
+    double tab[256];            // 2^(43 - j / 256)
     u64 wsum[kSampleWarps], wabove[kSampleWarps], wall[kSampleWarps];
     u64 gm[32];                 // group sums of a list's histogram
     u64 tiny[32];
@@ -144,11 +144,11 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
-// Fixed-point weight of a logit (mx: the row's largest).  2^(-(k + r) / 256)
-// with k = round(256 log2(e) (mx - l) / T): a table of 2^(-j / 256) and the
-// Taylor polynomial of 2^(-r / 256) to the fourth power (|r| <= 1/2: its
-// remainder is below 2^-53), so 11 double operations.  A weight below the live
-// threshold comes out as garbage.
+// Fixed-point weight of a logit (mx: the row's largest, finite).
+// 2^(43 - (k + r) / 256) with k = round(256 log2(e) (mx - l) / T): a table of
+// 2^(43 - j / 256) and the Taylor polynomial of 2^(-r / 256) to the fourth
+// power (|r| <= 1/2: its remainder is below 2^-53), so 11 double operations.
+// A weight below the live threshold comes out as garbage.
 struct SampleWeight {
     float mx;
     double c;           // 256 log2(e) / T
@@ -165,22 +165,25 @@ struct SampleWeight {
         p = __fma_rn(r, p, -a);
         p = __fma_rn(r, p, 1.0);
         const double w = p * tab[k & 255];
-        const double s = __hiloint2double(__double2hiint(w) + ((43 - (k >> 8)) << 20), __double2loint(w));
-        const u64 f = (u64)__double_as_longlong(s + 4503599627370496.0) & 0xfffffffffffffull;  // + 2^52
-        return l == mx ? 1ull << 43 : f;
+        // the exponent falls by k / 256; adding 2^52 rounds to an integer in the low bits
+        const double s = __hiloint2double(__double2hiint(w) - (int)((unsigned)(k & ~255) << 12), __double2loint(w));
+        return (u64)__double_as_longlong(s + 4503599627370496.0) & 0xfffffffffffffull;
     }
 };
 
 // The histogram's bins: `scale` to a unit of mx - l, the last bin takes what
 // lies beyond.  Bin 0 holds the largest logits and the bin never falls as the
 // logit falls: every step is a monotone fp32 operation.  Adding 2^23 rounds to
-// an integer held in the low bits; the clamp takes the NaN of inf - inf or
-// 0 * inf to the last bin, where the row's other elements then are as well.
+// an integer held in the low bits; the clamp takes the NaN of 0 * inf (a
+// temperature whose scale overflows) to the last bin, where the row's other
+// elements then are as well.
 struct SampleBinning {
     float mx, scale;
+    __device__ __forceinline__ float place(float l) const {  // 2^23 + the bin
+        return fminf(__fmaf_rn(__fsub_rn(mx, l), scale, 8388608.f), 8388608.f + (kSampleBins - 1));
+    }
     __device__ __forceinline__ int operator()(float l) const {
-        const float v = fminf(__fmaf_rn(__fsub_rn(mx, l), scale, 8388608.f), 8388608.f + (kSampleBins - 1));
-        return __float_as_int(v) & (kSampleBins - 1);
+        return __float_as_int(place(l)) & (kSampleBins - 1);
     }
 };
 
@@ -675,7 +678,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
     float u = __ldg(a.u + row);
     u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
-    if (tid < 256) sh.tab[tid] = exp2(-tid / 256.0);
+    if (tid < 256) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 256.0);  // 2^43 ...
     for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.cnt[i] = 0;
     s.weight.c = 369.32993046757466 / t64;  // 256 log2(e)
     s.weight.tab = sh.tab;
@@ -685,8 +688,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
 #pragma unroll
     for (uint32_t p = 1; p < kSampleMaxCluster; ++p)
         if (p < CL) best = max(best, s.inbox[p].best);
-    const uint32_t key_max = (uint32_t)(best >> 32);
-    const float mx = key_logit(key_max);
+    float mx = key_logit((uint32_t)(best >> 32));
     if (mx == -INFINITY || greedy) {  // nothing to draw from, or greedy
         if (rank == 0 && tid == 0) {
             a.token[row] = mx == -INFINITY ? -1 : (int32_t)(0xffffffffu - (uint32_t)best);
@@ -694,6 +696,16 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
         }
         return;  // the whole cluster
     }
+    u64 own_best = own;
+    if (mx == INFINITY) {  // the infinite logits share the row: take them as 0 and the others as -inf
+        for (int i = tid; i < n; i += kSampleThreads) buf[i] = buf[i] == INFINITY ? 0.f : -INFINITY;
+        mx = 0.f;
+        const u64 zero = (u64)logit_key(0.f) << 32;
+        best = zero | (uint32_t)best;
+        own_best = (uint32_t)(own >> 32) == logit_key(INFINITY) ? zero | (uint32_t)own : 0;
+        __syncthreads();
+    }
+    const uint32_t key_max = (uint32_t)(best >> 32);
     s.weight.mx = s.bin.mx = mx;
 
     // threshold: the weight's cut-off, then each filter raises it
@@ -703,7 +715,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     if (min_p > 0.f) kmin = (u64)min(key_max, logit_key(__double2float_ru((double)mx + min_log) + 0.f)) << 32;
 
     auto write = [&](uint32_t index, float l, u64 z) {
-        const double w = l == mx ? 1.0 : exp(((double)l - (double)mx) / t64);
+        const double w = exp(((double)l - (double)mx) / t64);
         a.token[row] = (int32_t)index;
         if (a.prob) a.prob[row] = (float)(w * 8796093022208.0 / (double)z);  // 2^43
     };
@@ -712,7 +724,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
         s.bin.scale = (float)(kSampleBins / kSampleLive / t64);  // bins over the whole live range
         if (top_k <= kSampleShortK && top_k * 4 <= (int)CL * kSampleThreads) {
             __syncthreads();
-            if (own >= kt) atomicAdd(&sh.cnt[s.bin(key_logit((uint32_t)(own >> 32)))], 1u);
+            if (own_best >= kt) atomicAdd(&sh.cnt[s.bin(key_logit((uint32_t)(own_best >> 32)))], 1u);
             __syncthreads();
             sample_share<false>(s, 0.f);
             if (warp == 0) {  // the bin of the k-th largest maximum, the last bin when there are fewer
@@ -870,6 +882,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
         };
         const float thr_l = key_logit((uint32_t)(thr >> 32)), kt_l = key_logit((uint32_t)(kt >> 32));
         const uint32_t thr_w = (uint32_t)thr, kt_w = (uint32_t)kt;
+        const float first = 8388608.f + (float)w0, last = 8388608.f + (float)w1;
         const bool kept = !window || thr > kt;  // else it comes out of the other sums
 #pragma unroll 1
         for (int i = s0 + 4 * lane; i < s1; i += 128) {  // four elements in flight
@@ -880,20 +893,31 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
             for (int c = 0; c < 4; ++c) w[c] = s.weight(l[c]);
             if (kept)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mk += s.at_least(l[c], i + c, thr_l, thr_w) ? w[c] : 0;
-            if (window)
+                for (int c = 0; c < 4; ++c)
+                    if (s.at_least(l[c], i + c, thr_l, thr_w)) mk += w[c];
+            if (window) {
+                bool live[4], in[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) live[c] = l[c] >= kt_l;
+                if (kt_w)  // the threshold lies inside a run of equals
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) live[c] = s.at_least(l[c], i + c, kt_l, kt_w);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const bool live = s.at_least(l[c], i + c, kt_l, kt_w);
-                    const int b = s.bin(l[c]);
-                    mt += live ? w[c] : 0;
-                    ma += live && b < w0 ? w[c] : 0;
-                    if (live && b >= w0 && b <= w1) {
-                        const uint32_t at = atomicAdd(&sh.sent, 1u);
-                        if (at < kSampleList) sh.list[at] = s.composite(i + c);  // sent below, by all threads
-                        else send(base + at, s.composite(i + c));
-                    }
+                    const float place = s.bin.place(l[c]);
+                    if (live[c]) mt += w[c];
+                    if (live[c] && place < first) ma += w[c];
+                    in[c] = live[c] && place >= first && place <= last;
                 }
+                if (in[0] || in[1] || in[2] || in[3])
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (in[c]) {
+                            const uint32_t at = atomicAdd(&sh.sent, 1u);
+                            if (at < kSampleList) sh.list[at] = s.composite(i + c);  // sent below, by all threads
+                            else send(base + at, s.composite(i + c));
+                        }
+            }
         }
         mk = warp_sum(mk);
         if (window) {
