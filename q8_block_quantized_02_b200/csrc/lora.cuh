@@ -177,18 +177,26 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
     for (int i = tid; i < tasks * V; i += kLoraThreads) sh.part[i] = 0.f;
     for (int64_t c0 = k0; c0 < k1; c0 += a.chunk) {
         const int units = (int)min((int64_t)a.chunk, k1 - c0) / 8;
-        // units of 8 columns of the rows of a task's group
-        auto load = [&](Lora8<T>(&w)[RB], int g, int un) {
-            const T *row = A + (int64_t)(g * RB) * a.K + c0 + 8 * un;
+        // unit `un` of 8 columns of a task's rows; past the last unit and the last
+        // row the last ones again, whose products are not used
+        const T *rows = nullptr;
+        uint32_t off[RB];
+        auto set_task = [&](int task) {
+            const int g = task / ks;
+            rows = A + (int64_t)(g * RB) * a.K + c0;
 #pragma unroll
-            for (int j = 0; j < RB; ++j) {
-                w[j].zero();
-                if (un < units && g * RB + j < r) w[j].load(row + j * a.K);
-            }
+            for (int j = 0; j < RB; ++j) off[j] = (uint32_t)min(j, r - 1 - g * RB) * (uint32_t)(a.K * ES);
         };
-        Lora8<T> cur[RB], nxt[RB];
-        int g = warp / ks, u0 = (warp % ks) * 32 + lane;
-        if (warp < tasks) load(cur, g, u0);  // on its way while x is staged
+        auto load = [&](Lora8<T>(&w)[RB], int un) {
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(rows + 8 * min(un, units - 1));
+#pragma unroll
+            for (int j = 0; j < RB; ++j) w[j].load(reinterpret_cast<const T *>(p + off[j]));
+        };
+        Lora8<T> even[RB], odd[RB];
+        if (warp < tasks) {  // on its way while x is staged
+            set_task(warp);
+            load(even, (warp % ks) * 32 + lane);
+        }
         __syncthreads();  // (x of the last chunk is no longer read)
         for (int i = tid; i < NT * units * 2; i += kLoraThreads) {
             const int t = i / (units * 2), q = i % (units * 2);
@@ -197,41 +205,46 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
                        : make_ulonglong2(0, 0);
         }
         __syncthreads();
+#pragma unroll 1
         for (int task = warp; task < tasks; task += kLoraWarps) {
             uint64_t acc2[V];  // even and odd columns
 #pragma unroll
             for (int i = 0; i < V; ++i) acc2[i] = 0;
-            const int next_g = (task + kLoraWarps) / ks, next_u0 = ((task + kLoraWarps) % ks) * 32 + lane;
-            for (int un = u0; un - lane < units; un += ks * 32) {
-                // the next columns, or the next task's first
-                const bool more = un - lane + ks * 32 < units;
-                load(nxt, more ? g : next_g, more ? un + ks * 32 : next_u0);
-                if (un < units) {
-                    ulonglong2 x[NT][2];
+            auto multiply = [&](const Lora8<T>(&a8)[RB], int un) {
+                if (un >= units) return;
+                ulonglong2 x[NT][2];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        x[t][0] = xs[(t * 2) * half + un];
-                        x[t][1] = xs[(t * 2 + 1) * half + un];
-                    }
-#pragma unroll
-                    for (int j = 0; j < RB; ++j) {
-                        uint64_t w[4];
-                        cur[j].get(w);
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            uint64_t &v = acc2[j * NT + t];
-                            v = fma_f32x2(w[0], x[t][0].x, v);
-                            v = fma_f32x2(w[1], x[t][0].y, v);
-                            v = fma_f32x2(w[2], x[t][1].x, v);
-                            v = fma_f32x2(w[3], x[t][1].y, v);
-                        }
-                    }
+                for (int t = 0; t < NT; ++t) {
+                    x[t][0] = xs[(t * 2) * half + un];
+                    x[t][1] = xs[(t * 2 + 1) * half + un];
                 }
 #pragma unroll
-                for (int j = 0; j < RB; ++j) cur[j] = nxt[j];
+                for (int j = 0; j < RB; ++j) {
+                    uint64_t w[4];
+                    a8[j].get(w);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        uint64_t &v = acc2[j * NT + t];
+                        v = fma_f32x2(w[0], x[t][0].x, v);
+                        v = fma_f32x2(w[1], x[t][0].y, v);
+                        v = fma_f32x2(w[2], x[t][1].x, v);
+                        v = fma_f32x2(w[3], x[t][1].y, v);
+                    }
+                }
+            };
+            const int step = ks * 32;
+            int un = (task % ks) * 32 + lane;
+            if (task != warp) {
+                set_task(task);
+                load(even, un);
             }
-            g = next_g;
-            u0 = next_u0;
+#pragma unroll 1
+            for (; un - lane < units; un += 2 * step) {  // two buffers in turn
+                if (un - lane + step < units) load(odd, un + step);
+                multiply(even, un);
+                if (un - lane + 2 * step < units) load(even, un + 2 * step);
+                multiply(odd, un + step);
+            }
             float acc[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = lora_sum2(acc2[i]);

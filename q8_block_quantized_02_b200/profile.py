@@ -6,6 +6,9 @@
     python -m q8_block_quantized_02_b200.profile --op moe --T 1
     python -m q8_block_quantized_02_b200.profile --op readpeak
     python -m q8_block_quantized_02_b200.profile --op decode --reps 3
+    python -m q8_block_quantized_02_b200.profile --op lora --M 3584 --K 18944 --N 16 --R 128
+    python -m q8_block_quantized_02_b200.profile --op route --T 4096 --E 256 --k 8
+    python -m q8_block_quantized_02_b200.profile --op sample --M 152064 --N 16 --filter nucleus
 
 Weights follow the synthetic Q8_0 recipe (q uniform in [-127, 127], d =
 |N(0,1)| * 0.02) and activations are N(0,1).  Enough packed copies of the
@@ -33,6 +36,13 @@ benchmark's step: 24 x {qkv, wo, gate_up + SwiGLU, down} + lm_head, 97
 dependent launches on one stream), eagerly, after `--warmup` steps: the
 driver of ncu captures of the decode kernels in their chain.
 
+`--op lora` times q8_lora (adapters of rank R in bf16, one per activation row,
+on an M x K projection), `--op route` q8_moe_route_grouped (T tokens, E experts
+in 8 groups, sigmoid scores, top-k), `--op sample` q8_sample (N rows of M
+logits ~ N(0,1), `--filter` topk = top-k 50 with top-p 0.95 and min-p 0.05,
+nucleus = top-p 0.9).  `--copies` sets of inputs are walked through (default:
+enough to cover three times the L2 cache for lora, else 8).
+
 `--op readpeak` is a reference figure, not a libq8 product: the HBM read rate
 of a plain reduction (torch.sum over 4 GiB of fp32, so every byte is read
 once and nothing is written back), the read-only counterpart of the measured
@@ -53,7 +63,7 @@ if ROOT not in sys.path:
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--op", choices=["gemv", "argmax", "swiglu", "q8q8", "q4k", "q6k", "q6kp", "moe", "readpeak",
-                             "decode"],
+                             "decode", "lora", "route", "sample"],
                     default="gemv",
                     help="q8_gemv, q8_gemv_argmax (logits not written), q8_gate_up_swiglu (M = rows of "
                          "the stacked gate|up matrix) or q8_quantize_act + q8q8_gemv (only q8q8_gemv is "
@@ -73,10 +83,14 @@ def main(argv=None) -> int:
     ap.add_argument("--I", type=int, default=1408, help="moe: expert intermediate size")
     ap.add_argument("--Is", type=int, default=5632, help="moe: shared expert intermediate size (0: none)")
     ap.add_argument("--k", type=int, default=4, help="moe: experts per token")
+    ap.add_argument("--R", type=int, default=64, help="lora: rank")
+    ap.add_argument("--filter", choices=["topk", "nucleus"], default="topk", help="sample: which filters are on")
     ap.add_argument("--routings", type=int, default=16, help="moe: distinct routings cycled through")
     args = ap.parse_args(argv)
     if args.op == "moe":
         return _moe(args)
+    if args.op in ("lora", "route", "sample"):
+        return _request(args)
     if args.op == "readpeak":
         return _readpeak(args)
     if args.op == "decode":
@@ -231,6 +245,61 @@ def _decode(args) -> int:
     us = t0.elapsed_time(t1) * 1e3 / max(1, args.reps)
     print(json.dumps({"op": "decode", "launches_per_step": len(specs), "us_per_step_eager": round(us, 2),
                       "reps": args.reps, "device_error": word}), flush=True)
+    return 0 if st == 0 else 1
+
+
+def _request(args) -> int:
+    import torch
+
+    import q8_block_quantized_02_b200 as q8
+
+    dev = torch.device("cuda", torch.cuda.current_device())
+    g = torch.Generator(device=dev).manual_seed(args.seed)
+    M, K, N, R = args.M, args.K, args.N, args.R
+    rand = lambda *s: torch.randn(*s, generator=g, device=dev)
+    calls, out = [], {"op": args.op}
+    if args.op == "lora":
+        nbytes = N * R * (M + K) * 2
+        l2 = torch.cuda.get_device_properties(dev).L2_cache_size
+        copies = args.copies or max(2, -(-3 * l2 // nbytes))
+        x, y, adapter = rand(N, K), torch.empty(N, M, device=dev), torch.arange(N, dtype=torch.int32, device=dev)
+        for _ in range(copies):
+            A, B = rand(N, R, K).bfloat16(), rand(N, M, R).bfloat16()
+            calls.append(lambda A=A, B=B: q8.q8_lora(x, A, B, None, None, adapter, None, y, M, K, N, N, R, q8.Q8_BF16))
+        out |= {"M": M, "K": K, "N": N, "R": R, "bytes": nbytes}
+    elif args.op == "route":
+        T, E, k = args.T, args.E, args.k
+        copies = args.copies or 8
+        idx, w = torch.empty(T, k, dtype=torch.int32, device=dev), torch.empty(T, k, device=dev)
+        bias = rand(E) * 0.05
+        for _ in range(copies):
+            l = rand(T, E)
+            calls.append(lambda l=l: q8.q8_moe_route_grouped(l, bias, T, E, k, 8, 4, 2, q8.Q8_SCORE_SIGMOID, 1, 2.5, idx, w))
+        out |= {"T": T, "E": E, "k": k, "bytes": 4 * T * E + 8 * T * k}
+    else:
+        copies = args.copies or 8
+        token, prob = torch.empty(N, dtype=torch.int32, device=dev), torch.empty(N, device=dev)
+        full = lambda v, dt=torch.float32: torch.full((N,), v, dtype=dt, device=dev)
+        topk = args.filter == "topk"
+        tk, tp, mp = (full(50, torch.int32), full(0.95), full(0.05)) if topk else (None, full(0.9), None)
+        for _ in range(copies):
+            l, u = rand(N, M), torch.rand(N, generator=g, device=dev)
+            calls.append(lambda l=l, u=u: q8.q8_sample(l, None, tk, tp, mp, u, token, prob, N, M, M))
+        out |= {"V": M, "N": N, "filter": args.filter, "bytes": 4 * N * M}
+    for i in range(args.warmup):
+        calls[i % copies]()
+    torch.cuda.synchronize()
+    t0 = torch.cuda.Event(enable_timing=True)
+    t1 = torch.cuda.Event(enable_timing=True)
+    t0.record()
+    for i in range(args.reps):
+        calls[i % copies]()
+    t1.record()
+    torch.cuda.synchronize()
+    st, word = q8.q8_read_device_error()
+    us = t0.elapsed_time(t1) * 1e3 / max(1, args.reps)
+    print(json.dumps(out | {"us_per_call": round(us, 3), "GBps": round(out["bytes"] / us / 1e3, 1), "copies": copies,
+                            "reps": args.reps, "device_error": word}), flush=True)
     return 0 if st == 0 else 1
 
 
