@@ -211,10 +211,11 @@ inline q8_status encode_map_3d(CUtensorMap *map, CUtensorMapDataType dtype, cons
 // launches (programmatic dependent launch on the given stream)
 // ---------------------------------------------------------------------------
 // `cluster_x` > 1 groups consecutive CTAs along x into thread-block clusters.
+// `early`: the kernel may become resident before the previous one on the
+// stream has finished (programmatic dependent launch).
 template <typename... KArgs, typename... Args>
-inline q8_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                    cudaStream_t stream, const char *name, unsigned cluster_x,
-                                    Args &&...args) {
+inline q8_status launch_cluster(bool early, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t stream, const char *name, unsigned cluster_x, Args &&...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -222,7 +223,7 @@ inline q8_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 bl
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[0].val.programmaticStreamSerializationAllowed = early ? 1 : 0;
     int n = 1;
     if (cluster_x > 1) {
         attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -236,6 +237,12 @@ inline q8_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 bl
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     if (e != cudaSuccess) return cuda_fail(e, name);
     return Q8_OK;
+}
+
+template <typename... KArgs, typename... Args>
+inline q8_status launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t stream, const char *name, unsigned cluster_x, Args &&...args) {
+    return launch_cluster(true, kernel, grid, block, smem, stream, name, cluster_x, std::forward<Args>(args)...);
 }
 
 template <typename... KArgs, typename... Args>

@@ -975,24 +975,31 @@ static int cluster_for(int slot, int64_t n, const void *kernel, int threads, siz
 
 // A cluster per token, of the most CTAs with which the clusters of all tokens
 // run at once.
-static q8_status run_lora(LoraArgs a, int dtype, cudaStream_t stream) {
+static q8_status run_lora(LoraArgs a, int dtype, cudaStream_t stream, bool early) {
     const DeviceInfo *dev = nullptr;
     Q8_CHECK(device_info(&dev));
     const LoraKernel kern = lora_kernel_for(dtype);
     const int cl = cluster_for(dtype, a.N, reinterpret_cast<const void *>(kern), kLoraThreads,
                                lora_smem_bytes(kLoraChunk, kLoraTok), dev->sms, 16, kLoraMinCluster);
     a.chunk = (int)std::min<int64_t>(kLoraChunk, round_up(ceil_div(a.K / 32, cl) * 32, 256));
-    return launch_pdl_cluster(kern, dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), lora_smem_bytes(a.chunk, a.N), stream,
-                              "q8_lora launch", (unsigned)cl, a);
+    return launch_cluster(early, kern, dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), lora_smem_bytes(a.chunk, a.N),
+                          stream, "q8_lora launch", (unsigned)cl, a);
 }
 
 // The adapters write y = residual + their part; the projection's store then
-// adds its product to y in place.
+// adds its product to y in place.  Beside a large projection the adapters'
+// kernel does not become resident early: its clusters would take SMs as the
+// kernel before leaves them, spread over the GPU, and the projection's clusters
+// then find room later (3584x18944, N = 16, rank 128: 87.7 us early, 80.4 not;
+// N = 4, rank 64: 59.0 and 58.1).  Beside a small one its launch latency counts
+// for more (896x4864, N = 1: 9.1 us early, 9.8 not; 3584x3584, N = 12: 54.5
+// and 54.8).
+constexpr int64_t kLoraEarlyMax = 16384;  // M + K below which it is launched early
 static q8_status run_gemv_lora(const void *W, const LoraArgs &a, int64_t N, int64_t n_adapters, int64_t R, int dtype,
                                cudaStream_t stream, bool split) {
     Q8_CHECK(lora_check(a, N, n_adapters, R, dtype));
     Q8_CHECK(check_device_ptr(W));
-    Q8_CHECK(run_lora(a, dtype, stream));
+    Q8_CHECK(run_lora(a, dtype, stream, a.M + a.K < kLoraEarlyMax));
     return run_tile(W, a.x, nullptr, a.y, a.M, a.K, N, kModeF32, stream, nullptr, a.y, split);
 }
 
@@ -1319,7 +1326,7 @@ q8_status q8_lora(const float *x, const void *A, const void *B, const int32_t *r
                   int64_t n_adapters, int64_t R, int dtype, q8_stream_t stream) {
     const LoraArgs a{x, A, B, rank, scale, adapter, residual, y, M, K, (int)N, (int)n_adapters, (int)R, 0};
     Q8_CHECK(lora_check(a, N, n_adapters, R, dtype));
-    return run_lora(a, dtype, (cudaStream_t)stream);
+    return run_lora(a, dtype, (cudaStream_t)stream, true);
 }
 
 q8_status q8_gemv_lora(const void *W, const float *x, const void *A, const void *B, const int32_t *rank,

@@ -1,7 +1,9 @@
 // route_grouped.cuh -- MoE router with softmax or sigmoid scores, a selection
 // bias, expert groups and scaled weights.  One warp per token.  Scores are
 // doubles: a pick is decided between scores that lie next to each other, and
-// fp32 scores would tie or swap where the definition does not.
+// fp32 scores would tie or swap where the definition does not.  They are
+// compared as 64-bit integers of the same order, which costs no double
+// operations.
 #pragma once
 
 #include "q8_device.cuh"
@@ -29,10 +31,12 @@ __device__ __forceinline__ unsigned long long ordered_key(double v) {
     return (b >> 63) ? ~b : b | (1ull << 63);
 }
 
-__device__ __forceinline__ double nan_to_ninf(double v) { return isnan(v) ? -INFINITY : v; }
+__device__ __forceinline__ double key_double(unsigned long long k) {
+    return __longlong_as_double((long long)((k >> 63) ? k & ~(1ull << 63) : ~k));
+}
 
 __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const RouteArgs a) {
-    __shared__ double sel_s[kRouteGWarps][kRouteMaxE + 32];  // selection scores by group
+    __shared__ unsigned long long sel_s[kRouteGWarps][kRouteMaxE + 32];  // selection keys by group
     __shared__ double score_s[kRouteGWarps][kRouteMaxE];
     constexpr int PL = kRouteMaxE / 32;  // experts per lane
     pdl_wait_and_trigger();
@@ -77,30 +81,29 @@ __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const 
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
         const int e = lane + 32 * i;
-        const double c = e < a.E ? nan_to_ninf(s[i] + (a.bias ? (double)__ldg(a.bias + e) : 0.0)) : 0.0;
-        key[i] = e < a.E ? ordered_key(c) : 0ull;
+        key[i] = e < a.E ? ordered_key(s[i] + (a.bias ? (double)__ldg(a.bias + e) : 0.0)) : 0ull;
         if (e < a.E) {
             score_s[warp][e] = s[i];
-            if (a.groups > 1) sel_s[warp][e + (e * inv >> 16) * lpg] = c;
+            if (a.groups > 1) sel_s[warp][e + (e * inv >> 16) * lpg] = key[i];
         }
     }
     __syncwarp();
     if (a.groups > 1) {
         const int g = lane / lpg, sub = lane % lpg;
-        double b0 = -INFINITY, b1 = -INFINITY;  // the two largest
+        unsigned long long b0 = 0, b1 = 0;  // the two largest
         if (g < a.groups)
             for (int e = sub; e < size; e += lpg) {
-                const double c = sel_s[warp][g * (size + lpg) + e];
-                b1 = c > b0 ? b0 : fmax(b1, c);
-                b0 = fmax(b0, c);
+                const unsigned long long c = sel_s[warp][g * (size + lpg) + e];
+                b1 = max(b1, min(b0, c));
+                b0 = max(b0, c);
             }
         for (int off = lpg >> 1; off > 0; off >>= 1) {
-            const double o0 = __shfl_xor_sync(0xffffffffu, b0, off);
-            const double o1 = __shfl_xor_sync(0xffffffffu, b1, off);
-            b1 = fmax(fmin(b0, o0), fmax(b1, o1));
-            b0 = fmax(b0, o0);
+            const unsigned long long o0 = __shfl_xor_sync(0xffffffffu, b0, off);
+            const unsigned long long o1 = __shfl_xor_sync(0xffffffffu, b1, off);
+            b1 = max(min(b0, o0), max(b1, o1));
+            b0 = max(b0, o0);
         }
-        const unsigned long long gk = ordered_key(a.group_top == 2 ? b0 + b1 : b0);
+        const unsigned long long gk = a.group_top == 2 ? ordered_key(key_double(b0) + key_double(b1)) : b0;
         int better = 0;
         for (int o = 0; o < a.groups; ++o) {
             const unsigned long long ok = __shfl_sync(0xffffffffu, gk, o * lpg);
@@ -126,8 +129,14 @@ __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const 
             }
         const unsigned hi = (unsigned)(bk >> 32), lo = (unsigned)bk;
         const unsigned mh = __reduce_max_sync(0xffffffffu, hi);
-        const unsigned ml = __reduce_max_sync(0xffffffffu, hi == mh ? lo : 0u);
-        const unsigned e = __reduce_min_sync(0xffffffffu, hi == mh && lo == ml ? (unsigned)(lane + 32 * bi) : ~0u);
+        const unsigned at = __ballot_sync(0xffffffffu, hi == mh);
+        unsigned e;
+        if ((at & (at - 1)) == 0) {  // nearly always: one lane has the largest high word
+            e = __shfl_sync(0xffffffffu, (unsigned)(lane + 32 * bi), __ffs(at) - 1);
+        } else {
+            const unsigned ml = __reduce_max_sync(0xffffffffu, hi == mh ? lo : 0u);
+            e = __reduce_min_sync(0xffffffffu, hi == mh && lo == ml ? (unsigned)(lane + 32 * bi) : ~0u);
+        }
         if ((e & 31u) == (unsigned)lane) {
 #pragma unroll
             for (int i = 0; i < PL; ++i)
