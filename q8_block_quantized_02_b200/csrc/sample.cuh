@@ -70,6 +70,7 @@ struct alignas(16) SampleInbox {
     u64 best;                      // largest composite key
     u64 above, all, kept;          // masses of the pass over the weights
     uint32_t sent;                 // elements of the short list
+    uint16_t pulled[kSampleGroup]; // (of this CTA's own) the bins' counts of a group in that CTA
 };
 
 struct alignas(16) SampleShared {
@@ -80,11 +81,12 @@ struct alignas(16) SampleShared {
     u64 mass[kSampleBins];
     u64 list[kSampleList];
     uint32_t cnt[kSampleBins];  // read by the cluster
-    double tab[256];            // 2^(43 - j / 256)
+    double tab[128];            // 2^(43 - j / 128)
     u64 wsum[kSampleWarps], wabove[kSampleWarps], wall[kSampleWarps];
     u64 gm[32];                 // group sums of a list's histogram
     u64 tiny[32];
     uint32_t tiny_n;
+    uint32_t span[2];           // least and largest key of a list
     uint32_t sent;              // elements this CTA has put into a list
     uint32_t short_n;           // rank 0: places of the short list given out
     // results of one thread or warp for the whole CTA
@@ -144,18 +146,24 @@ __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
+__device__ __forceinline__ u64 warp_max(u64 v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
 // Fixed-point weight of a logit (mx: the row's largest, finite).
-// 2^(43 - (k + r) / 256) with k = round(256 log2(e) (mx - l) / T): a table of
-// 2^(43 - j / 256) and the Taylor polynomial of 2^(-r / 256) to the fourth
-// power (|r| <= 1/2: its remainder is below 2^-53), so 11 double operations.
+// 2^(43 - (k + r) / 128) with k = round(128 log2(e) (mx - l) / T): a table of
+// 2^(43 - j / 128) and the Taylor polynomial of 2^(-r / 128) to the fourth
+// power (|r| <= 1/2: its remainder is below 2^-49), so 11 double operations.
 // A weight below the live threshold comes out as garbage.
 struct SampleWeight {
     float mx;
-    double c;           // 256 log2(e) / T
+    double c;           // 128 log2(e) / T
     const double *tab;  // in shared memory
     __device__ __forceinline__ u64 operator()(float l) const {
         constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52
-        constexpr double a = 0.0027076061740622863;    // ln 2 / 256
+        constexpr double a = 0.0054152123481245727;    // ln 2 / 128
         const double d = (double)mx - (double)l;
         const double t = __fma_rn(d, c, kMagic);
         const int k = __double2loint(t);
@@ -164,9 +172,9 @@ struct SampleWeight {
         p = __fma_rn(r, p, a * a / 2);
         p = __fma_rn(r, p, -a);
         p = __fma_rn(r, p, 1.0);
-        const double w = p * tab[k & 255];
-        // the exponent falls by k / 256; adding 2^52 rounds to an integer in the low bits
-        const double s = __hiloint2double(__double2hiint(w) - (int)((unsigned)(k & ~255) << 12), __double2loint(w));
+        const double w = p * tab[k & 127];
+        // the exponent falls by k / 128; adding 2^52 rounds to an integer in the low bits
+        const double s = __hiloint2double(__double2hiint(w) - (int)((unsigned)(k & ~127) << 13), __double2loint(w));
         return (u64)__double_as_longlong(s + 4503599627370496.0) & 0xfffffffffffffull;
     }
 };
@@ -241,34 +249,31 @@ __device__ bool sample_list_select(const SampleRow &s, bool window, int n, u64 b
     u64 lo = 0, hi = ~0ull;
     bool first = true;
     if (count > 32) {
-        u64 mn = ~0ull, mxv = 0;
+        // the keys it spans
+        uint32_t mn = ~0u, mxv = 0;
         for (int i = s.tid; i < n; i += kSampleThreads) {
-            const u64 e = list[i];
-            mn = min(mn, e);
-            mxv = max(mxv, e);
+            const uint32_t k = (uint32_t)(list[i] >> 32);
+            mn = min(mn, k);
+            mxv = max(mxv, k);
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-            mxv = max(mxv, __shfl_xor_sync(0xffffffffu, mxv, off));
-        }
-        if (s.lane == 0) {
-            sh.gm[s.warp] = mn;
-            sh.gm[16 + s.warp] = mxv;
+        mn = __reduce_min_sync(0xffffffffu, mn);
+        mxv = __reduce_max_sync(0xffffffffu, mxv);
+        if (s.tid == 0) {
+            sh.span[0] = ~0u;
+            sh.span[1] = 0;
         }
         for (int i = s.tid; i < 1024; i += kSampleThreads) {
             sh.cnt[i] = 0;
             if (MASS) mass[i] = 0;
         }
         __syncthreads();
-        lo = sh.gm[0];
-        hi = sh.gm[16];
-#pragma unroll
-        for (int w = 1; w < kSampleWarps; ++w) {
-            lo = min(lo, sh.gm[w]);
-            hi = max(hi, sh.gm[16 + w]);
+        if (s.lane == 0) {
+            atomicMin(&sh.span[0], mn);
+            atomicMax(&sh.span[1], mxv);
         }
         __syncthreads();
+        lo = (u64)sh.span[0] << 32;
+        hi = (u64)sh.span[1] << 32 | 0xffffffffu;
     }
     while (count > 32) {
         const int bits = 64 - __clzll((long long)(hi - lo));
@@ -425,27 +430,30 @@ __device__ __forceinline__ void sample_share(const SampleRow &s, float est) {
     cluster_sync_all();
 }
 
-// The counts of the 64 bins of group g (lane's bins: 64 g + lane and + 32), of
-// all CTAs and of those of lower rank.
-__device__ __forceinline__ void sample_pull_counts(const SampleRow &s, int g, uint32_t (&c)[2], uint32_t (&lower)[2]) {
+// The counts of the 64 bins of group g from all CTAs, into the inboxes' pulled.
+// Whole CTA.
+__device__ __forceinline__ void sample_pull_counts(const SampleRow &s, int g) {
+    static_assert(kSampleThreads % kSampleGroup == 0, "a thread keeps to one bin");
+    const int bin = s.tid % kSampleGroup;
+#pragma unroll 1
+    for (uint32_t p = s.tid / kSampleGroup; p < s.CL; p += kSampleThreads / kSampleGroup)
+        s.inbox[p].pulled[bin] = (uint16_t)ld_cluster_u32(map_to_rank(smem_u32(&s.sh->cnt[g * kSampleGroup + bin]), p));
+    __syncthreads();
+}
+// Sums of what was pulled: lane's bins 64 g + lane and + 32, of all CTAs and of
+// those of lower rank.
+__device__ __forceinline__ void sample_sum_counts(const SampleRow &s, uint32_t (&c)[2], uint32_t (&lower)[2]) {
     c[0] = c[1] = lower[0] = lower[1] = 0;
-    uint32_t v[2][kSampleMaxCluster];
-#pragma unroll
-    for (uint32_t p = 0; p < kSampleMaxCluster; ++p) {
-        v[0][p] = v[1][p] = 0;
-        if (p < s.CL) {
-            const uint32_t a = map_to_rank(smem_u32(&s.sh->cnt[g * kSampleGroup + s.lane]), p);
-            v[0][p] = ld_cluster_u32(a);
-            v[1][p] = ld_cluster_u32(a + 128);
+#pragma unroll 2
+    for (uint32_t p = 0; p < s.CL; ++p) {
+        const uint32_t x = s.inbox[p].pulled[s.lane], y = s.inbox[p].pulled[s.lane + 32];
+        if (p == s.rank) {
+            lower[0] = c[0];
+            lower[1] = c[1];
         }
+        c[0] += x;
+        c[1] += y;
     }
-#pragma unroll
-    for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            c[h] += v[h][p];
-            if (p < s.rank) lower[h] += v[h][p];
-        }
 }
 
 // One filter, exactly: the threshold composite key in [lo, hi] of a count (the
@@ -465,35 +473,42 @@ __device__ bool sample_filter(const SampleRow &s, u64 lo, u64 hi, u64 target, do
             sample_histogram<MASS, false>(s, lo, hi, shift);
         if (s.tid == 0) sh.sent = 0;
         sample_share<MASS>(s, 0.f);
-        if (s.warp == 0) {  // the crossing group, then its bins from all CTAs
+        // the crossing group, then its bins from all CTAs
+        int b = -1, g = -1;
+        uint32_t bc = 0, off = 0;
+        u64 b4 = before;
+        if (s.warp == 0) {
             u64 v = 0;
-#pragma unroll
-            for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
-                if (p < s.CL) v += MASS ? s.inbox[p].gmass[s.lane] : s.inbox[p].gcnt[s.lane];
+#pragma unroll 2
+            for (uint32_t p = 0; p < s.CL; ++p) v += MASS ? s.inbox[p].gmass[s.lane] : s.inbox[p].gcnt[s.lane];
             const u64 inc = warp_incl_scan(v, s.lane);
             const u64 all = __shfl_sync(0xffffffffu, inc, 31);
             if (MASS && it == 0) {
                 target = (u64)ceil(top_p * (double)all);
                 if (target < 1) target = 1;
             }
-            int b = -1;
-            uint32_t bc = 0, off = 0;
-            u64 b4 = before + all;
             if (target <= before + all) {
                 const unsigned cross = __ballot_sync(0xffffffffu, before + inc - v < target && target <= before + inc);
-                const int g = __ffs(cross) - 1;
+                g = __ffs(cross) - 1;
                 b4 = before + __shfl_sync(0xffffffffu, inc - v, g);
+            }
+            if (s.lane == 0) sh.bin = g;
+        }
+        __syncthreads();
+        if (sh.bin < 0) return false;
+        sample_pull_counts(s, sh.bin);
+        if (s.warp == 0) {
+            {
                 uint32_t fc[2], fl[2];
                 u64 fm[2] = {0, 0};
-                sample_pull_counts(s, g, fc, fl);
+                sample_sum_counts(s, fc, fl);
                 if (MASS) {
-#pragma unroll
-                    for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
-                        if (p < s.CL) {
-                            const uint32_t am = map_to_rank(smem_u32(&sh.mass[g * kSampleGroup + s.lane]), p);
-                            fm[0] += ld_cluster_u64(am);
-                            fm[1] += ld_cluster_u64(am + 256);
-                        }
+#pragma unroll 4
+                    for (uint32_t p = 0; p < s.CL; ++p) {
+                        const uint32_t am = map_to_rank(smem_u32(&sh.mass[g * kSampleGroup + s.lane]), p);
+                        fm[0] += ld_cluster_u64(am);
+                        fm[1] += ld_cluster_u64(am + 256);
+                    }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -535,9 +550,9 @@ __device__ bool sample_filter(const SampleRow &s, u64 lo, u64 hi, u64 target, do
             }
         }
         __syncthreads();
-        const int b = sh.bin;
-        if (b < 0) return false;
-        const uint32_t bc = sh.count, base = sh.base;
+        b = sh.bin;
+        bc = sh.count;
+        const uint32_t base = sh.base;
         before = sh.before;
         target = sh.target;
         const u64 nlo = sh.lo, nhi = sh.hi;  // (set when it > 0 or bc > kSampleList)
@@ -590,15 +605,10 @@ __device__ __forceinline__ u64 sample_scan(const SampleRow &s, u64 v, u64 *all) 
     __syncthreads();
     if (s.lane == 31) s.sh->wsum[s.warp] = inc;
     __syncthreads();
-    u64 b4 = 0, sum = 0;
-#pragma unroll
-    for (int w = 0; w < kSampleWarps; ++w) {
-        const u64 x = s.sh->wsum[w];
-        if (w < s.warp) b4 += x;
-        sum += x;
-    }
-    *all = sum;
-    return b4 + inc;
+    const u64 x = warp_incl_scan(s.lane < kSampleWarps ? s.sh->wsum[s.lane] : 0, s.lane);
+    *all = __shfl_sync(0xffffffffu, x, 31);
+    const u64 b4 = __shfl_sync(0xffffffffu, x, s.warp - 1 & 31);
+    return (s.warp ? b4 : 0) + inc;
 }
 
 // PER_SM: CTAs an SM is to hold (registers for one leave room for more
@@ -650,22 +660,19 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
             }
             for (int i = 4 * n4 + tid; i < n; i += kSampleThreads) buf[i] = take(__ldg(src + i), i);
         } else {
-#pragma unroll 8
+#pragma unroll 4
             for (int i = tid; i < n; i += kSampleThreads) buf[i] = take(__ldg(src + i), i);
         }
         if (tid < (-n & 3)) buf[n + tid] = -INFINITY;  // the last four are read together
         if (mi != 0x7fffffff) best = ((u64)logit_key(mv) << 32) | (0xffffffffu - (uint32_t)(i0 + mi));
     }
     const u64 own = best;  // this thread's largest
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, off));
+    best = warp_max(best);
     if (lane == 0) sh.wsum[warp] = best;
     __syncthreads();
-    if (tid < (int)CL) {
-        best = sh.wsum[0];
-#pragma unroll
-        for (int w = 1; w < kSampleWarps; ++w) best = max(best, sh.wsum[w]);
-        st_cluster_u64(map_to_rank(smem_u32(&s.inbox[rank].best), tid), best);
+    if (warp == 0) {
+        best = warp_max(lane < kSampleWarps ? sh.wsum[lane] : 0);
+        if (lane < (int)CL) st_cluster_u64(map_to_rank(smem_u32(&s.inbox[rank].best), lane), best);
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     // the row's parameters, while the barrier completes
@@ -678,16 +685,13 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
     float u = __ldg(a.u + row);
     u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
-    if (tid < 256) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 256.0);  // 2^43 ...
+    if (tid < 128) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 128.0);  // 2^43 ...
     for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.cnt[i] = 0;
-    s.weight.c = 369.32993046757466 / t64;  // 256 log2(e)
+    s.weight.c = 184.66496523378733 / t64;  // 128 log2(e)
     s.weight.tab = sh.tab;
     const double min_log = min_p > 0.f ? t64 * log((double)fminf(min_p, 1.f)) : 0.0;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    best = s.inbox[0].best;
-#pragma unroll
-    for (uint32_t p = 1; p < kSampleMaxCluster; ++p)
-        if (p < CL) best = max(best, s.inbox[p].best);
+    best = warp_max(lane < (int)CL ? s.inbox[lane].best : 0);
     float mx = key_logit((uint32_t)(best >> 32));
     if (mx == -INFINITY || greedy) {  // nothing to draw from, or greedy
         if (rank == 0 && tid == 0) {
@@ -727,19 +731,27 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
             if (own_best >= kt) atomicAdd(&sh.cnt[s.bin(key_logit((uint32_t)(own_best >> 32)))], 1u);
             __syncthreads();
             sample_share<false>(s, 0.f);
-            if (warp == 0) {  // the bin of the k-th largest maximum, the last bin when there are fewer
+            // the bin of the k-th largest maximum, the last bin when there are fewer
+            uint32_t above = 0;
+            if (warp == 0) {
                 uint32_t c = 0;
-#pragma unroll
-                for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
-                    if (p < CL) c += s.inbox[p].gcnt[lane];
+#pragma unroll 2
+                for (uint32_t p = 0; p < CL; ++p) c += s.inbox[p].gcnt[lane];
                 const uint32_t inc = warp_incl_scan(c, lane);
                 const unsigned cross = __ballot_sync(0xffffffffu, inc >= (uint32_t)top_k);
+                const int g = cross ? __ffs(cross) - 1 : -1;
+                above = __shfl_sync(0xffffffffu, inc - c, g & 31);
+                if (lane == 0) sh.bin = g;
+            }
+            __syncthreads();
+            const int g = sh.bin;
+            if (g >= 0) sample_pull_counts(s, g);
+            if (warp == 0) {
                 int b = kSampleBins - 1;
-                if (cross) {
-                    const int g = __ffs(cross) - 1;
+                if (g >= 0) {
                     uint32_t fc[2], unused[2];
-                    sample_pull_counts(s, g, fc, unused);
-                    const uint32_t c0 = __shfl_sync(0xffffffffu, inc - c, g) + warp_incl_scan(fc[0], lane);
+                    sample_sum_counts(s, fc, unused);
+                    const uint32_t c0 = above + warp_incl_scan(fc[0], lane);
                     const uint32_t c1 = __shfl_sync(0xffffffffu, c0, 31) + warp_incl_scan(fc[1], lane);
                     const unsigned at0 = __ballot_sync(0xffffffffu, c0 >= (uint32_t)top_k);
                     const unsigned at1 = __ballot_sync(0xffffffffu, c1 >= (uint32_t)top_k);
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
             // the elements down to that bin: gathered here, then sent to rank 0
             const int b = sh.bin;
             const float live = key_logit((uint32_t)(kt >> 32));
-#pragma unroll 4
+#pragma unroll 2
             for (int j = tid; 4 * j < n; j += kSampleThreads) {
                 const float4 q = reinterpret_cast<const float4 *>(buf)[j];
                 const float l[4] = {q.x, q.y, q.z, q.w};
@@ -819,26 +831,33 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
         sample_histogram<false, true>(s, kt, best, 0);
         if (tid == 0) sh.sent = 0;
         sample_share<false>(s, kEst);
+        float b4 = 0.f, goal = 0.f;
+        uint32_t ca = 0, la = 0;
+        int g = 0;
         if (warp == 0) {
             float e = 0.f;
             uint32_t c = 0, low = 0;
-#pragma unroll
-            for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
-                if (p < CL) {
-                    e += __uint_as_float((uint32_t)s.inbox[p].gmass[lane]);
-                    c += s.inbox[p].gcnt[lane];
-                    if (p < rank) low += s.inbox[p].gcnt[lane];
-                }
+#pragma unroll 2
+            for (uint32_t p = 0; p < CL; ++p) {
+                e += __uint_as_float((uint32_t)s.inbox[p].gmass[lane]);
+                if (p == rank) low = c;
+                c += s.inbox[p].gcnt[lane];
+            }
             const float inc = warp_incl_scan(e, lane);
             const uint32_t cinc = warp_incl_scan(c, lane);
-            const float goal = top_p * __shfl_sync(0xffffffffu, inc, 31);
+            goal = top_p * __shfl_sync(0xffffffffu, inc, 31);
             const unsigned cross = __ballot_sync(0xffffffffu, inc >= goal);
-            const int g = cross ? __ffs(cross) - 1 : kSampleGroups - 1;
-            float b4 = __shfl_sync(0xffffffffu, inc - e, g);
-            const uint32_t ca = __shfl_sync(0xffffffffu, cinc - c, g);
-            const uint32_t la = __shfl_sync(0xffffffffu, warp_incl_scan(low, lane) - low, g);
+            g = cross ? __ffs(cross) - 1 : kSampleGroups - 1;
+            b4 = __shfl_sync(0xffffffffu, inc - e, g);
+            ca = __shfl_sync(0xffffffffu, cinc - c, g);
+            la = __shfl_sync(0xffffffffu, warp_incl_scan(low, lane) - low, g);
+            if (lane == 0) sh.bin = g;
+        }
+        __syncthreads();
+        sample_pull_counts(s, sh.bin);
+        if (warp == 0) {
             uint32_t fc[2], fl[2];
-            sample_pull_counts(s, g, fc, fl);
+            sample_sum_counts(s, fc, fl);
             const int base = g * kSampleGroup;
             const float e0 = b4 + warp_incl_scan((float)fc[0] * exp2f(-kEst * (float)(base + lane)), lane);
             const float e1 = __shfl_sync(0xffffffffu, e0, 31) +
@@ -933,18 +952,17 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
         __syncthreads();
         if (window)
             for (int i = tid; i < (int)min(sh.sent, (uint32_t)kSampleList); i += kSampleThreads) send(base + i, sh.list[i]);
-        if (tid < (int)CL) {
-            mk = ma = mt = 0;
-#pragma unroll
-            for (int w = 0; w < kSampleWarps; ++w) {
-                mk += sh.wsum[w];
-                ma += sh.wabove[w];
-                mt += sh.wall[w];
+        if (warp == 0) {
+            const bool in = lane < kSampleWarps;
+            mk = warp_sum(in ? sh.wsum[lane] : 0);
+            ma = warp_sum(in ? sh.wabove[lane] : 0);
+            mt = warp_sum(in ? sh.wall[lane] : 0);
+            if (lane < (int)CL) {
+                const uint32_t box = map_to_rank(smem_u32(&s.inbox[rank]), lane);
+                st_cluster_u64(box + offsetof(SampleInbox, kept), mk);
+                st_cluster_u64(box + offsetof(SampleInbox, above), ma);
+                st_cluster_u64(box + offsetof(SampleInbox, all), mt);
             }
-            const uint32_t box = smem_u32(&s.inbox[rank]);
-            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, kept), tid), mk);
-            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, above), tid), ma);
-            st_cluster_u64(map_to_rank(box + offsetof(SampleInbox, all), tid), mt);
         }
         cluster_sync_all();
     };
@@ -955,13 +973,8 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     if (filter_p) {
         bool found = false;
         if (w1 >= 0) {
-            u64 above = 0, z = 0;
-#pragma unroll
-            for (uint32_t p = 0; p < kSampleMaxCluster; ++p)
-                if (p < CL) {
-                    above += s.inbox[p].above;
-                    z += s.inbox[p].all;
-                }
+            const u64 above = warp_sum(lane < (int)CL ? s.inbox[lane].above : 0);
+            const u64 z = warp_sum(lane < (int)CL ? s.inbox[lane].all : 0);
             u64 target = (u64)ceil((double)top_p * (double)z), cut;
             if (target < 1) target = 1;
             found = above < target && sample_list_select<true>(s, true, (int)n_list, above, target, &cut);
