@@ -365,7 +365,8 @@ typedef enum q8_score { Q8_SCORE_SOFTMAX = 0, Q8_SCORE_SIGMOID = 1 } q8_score;
  * and of experts, go to the lowest index.  w[t][j] = s[idx] (not c), divided
  * by the picks' sum when renormalize != 0, times scale.
  * Scores are held and compared in double, w is rounded once.  NaN logits count
- * as -inf; a score of -inf logits is 0, and +inf logits share a softmax; a NaN
+ * as -inf; a score of -inf logits is 0, and +inf logits share a softmax; an
+ * exponential below e^-708 is 0; a NaN
  * selection score (of a NaN bias, or of groups holding both infinities) counts
  * as -inf; w is 0 where the picks' sum is 0.  The picks are always top_k
  * different experts of the groups that stay.

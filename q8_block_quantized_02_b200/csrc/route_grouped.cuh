@@ -35,6 +35,34 @@ __device__ __forceinline__ double key_double(unsigned long long k) {
     return __longlong_as_double((long long)((k >> 63) ? k & ~(1ull << 63) : ~k));
 }
 
+// e^-x for x >= 0, 0 beyond 708 (whole warps): 2^(-(k + r) / 32) with k =
+// round(32 log2(e) x), a table of 2^(-j / 32) held one entry per lane and the
+// Taylor polynomial of 2^(-r / 32) to the sixth power (|r| <= 1/2: its
+// remainder is below 2^-57).
+__device__ __forceinline__ double exp_neg(double x, double tab) {
+    constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52
+    constexpr double a = 0.021660849392498290;     // ln 2 / 32
+    const double y = fmin(x, 709.0) * 46.166241308446828;  // 32 log2(e)
+    const double t = y + kMagic;
+    const int k = __double2loint(t);
+    const double r = y - (t - kMagic);
+    double p = __fma_rn(r, a * a * a * a * a * a / 720, -a * a * a * a * a / 120);
+    p = __fma_rn(r, p, a * a * a * a / 24);
+    p = __fma_rn(r, p, -a * a * a / 6);
+    p = __fma_rn(r, p, a * a / 2);
+    p = __fma_rn(r, p, -a);
+    p = __fma_rn(r, p, 1.0);
+    const double w = p * __shfl_sync(0xffffffffu, tab, k & 31);
+    return x > 708.0 ? 0.0 : __hiloint2double(__double2hiint(w) - ((k >> 5) << 20), __double2loint(w));
+}
+
+// 1 / d for 1 <= d: Newton's iteration from an fp32 estimate.
+__device__ __forceinline__ double reciprocal(double d) {
+    double y = (double)__fdividef(1.f, (float)d);
+    y = __fma_rn(y, __fma_rn(-d, y, 1.0), y);
+    return __fma_rn(y, __fma_rn(-d, y, 1.0), y);
+}
+
 __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const RouteArgs a) {
     __shared__ unsigned long long sel_s[kRouteGWarps][kRouteMaxE + 32];  // selection keys by group
     __shared__ double score_s[kRouteGWarps][kRouteMaxE];
@@ -52,9 +80,14 @@ __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const 
         if (isnan(v[i])) v[i] = -INFINITY;
     }
     double s[PL];
+    const double tab = exp2(-lane / 32.0);
     if (a.sigmoid) {
+        // 1 / (1 + e^-l), below 0 as e^l / (1 + e^l)
 #pragma unroll
-        for (int i = 0; i < PL; ++i) s[i] = lane + 32 * i < a.E ? 1.0 / (1.0 + exp(-(double)v[i])) : 0.0;
+        for (int i = 0; i < PL; ++i) {
+            const double z = exp_neg(fabs((double)v[i]), tab);
+            s[i] = (v[i] >= 0.f ? 1.0 : z) * reciprocal(1.0 + z);
+        }
     } else {
         float mx = -INFINITY;
 #pragma unroll
@@ -64,7 +97,8 @@ __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const 
         double z = 0.0;
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-            s[i] = v[i] == -INFINITY ? 0.0 : v[i] == mx ? 1.0 : exp((double)v[i] - (double)mx);
+            const double w = exp_neg((double)mx - (double)v[i], tab);
+            s[i] = v[i] == -INFINITY ? 0.0 : v[i] == mx ? 1.0 : w;
             z += s[i];
         }
 #pragma unroll
@@ -137,11 +171,9 @@ __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const 
             const unsigned ml = __reduce_max_sync(0xffffffffu, hi == mh ? lo : 0u);
             e = __reduce_min_sync(0xffffffffu, hi == mh && lo == ml ? (unsigned)(lane + 32 * bi) : ~0u);
         }
-        if ((e & 31u) == (unsigned)lane) {
+        const unsigned hit = (e & 31u) == (unsigned)lane ? 1u << (e >> 5) : 0u;  // (a bit, so that key stays in registers)
 #pragma unroll
-            for (int i = 0; i < PL; ++i)
-                if ((int)(e >> 5) == i) key[i] = 0ull;
-        }
+        for (int i = 0; i < PL; ++i) key[i] = (hit >> i) & 1u ? 0ull : key[i];
         if (lane == k) pick = (int)e;
     }
     double w = lane < a.top_k ? score_s[warp][pick] : 0.0;
