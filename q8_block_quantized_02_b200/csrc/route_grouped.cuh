@@ -24,13 +24,13 @@ struct RouteArgs {
     float scale;
 };
 
-// Order-preserving bits of a double, NaN as -inf, -0 as +0; above 0.
+// Order-preserving bits of a double, NaN as -inf, -0 as +0.  Their high word
+// is above 0 for every double.
 __device__ __forceinline__ unsigned long long ordered_key(double v) {
     v = isnan(v) ? -INFINITY : v + 0.0;
-    const unsigned long long b = (unsigned long long)__double_as_longlong(v);
-    return (b >> 63) ? ~b : b | (1ull << 63);
+    const int hi = __double2hiint(v), m = hi >> 31;
+    return (unsigned long long)((unsigned)hi ^ ((unsigned)m | 0x80000000u)) << 32 | ((unsigned)__double2loint(v) ^ (unsigned)m);
 }
-
 __device__ __forceinline__ double key_double(unsigned long long k) {
     return __longlong_as_double((long long)((k >> 63) ? k & ~(1ull << 63) : ~k));
 }
@@ -150,26 +150,33 @@ __global__ void __launch_bounds__(32 * kRouteGWarps) route_grouped_kernel(const 
             if (e < a.E && !((kept >> ((e * inv >> 16) * lpg)) & 1u)) key[i] = 0ull;
         }
     }
-    // top_k by key, ties to the lowest index
+    // top_k by key, ties to the lowest index.  One key nearly always has the
+    // largest high word alone, so a pick takes 32-bit maxima; the whole keys are
+    // compared where it does not.
     int pick = 0;
     for (int k = 0; k < a.top_k; ++k) {
-        unsigned long long bk = key[0];
-        int bi = 0;
+        unsigned mh = 0;
 #pragma unroll
-        for (int i = 1; i < PL; ++i)
-            if (key[i] > bk) {
-                bk = key[i];
-                bi = i;
-            }
-        const unsigned hi = (unsigned)(bk >> 32), lo = (unsigned)bk;
-        const unsigned mh = __reduce_max_sync(0xffffffffu, hi);
-        const unsigned at = __ballot_sync(0xffffffffu, hi == mh);
+        for (int i = 0; i < PL; ++i) mh = max(mh, (unsigned)(key[i] >> 32));
+        mh = __reduce_max_sync(0xffffffffu, mh);
+        unsigned mine = 0;  // which of this lane's keys have it
+#pragma unroll
+        for (int i = 0; i < PL; ++i) mine |= (unsigned)(key[i] >> 32) == mh ? 1u << i : 0u;
+        const unsigned at = __ballot_sync(0xffffffffu, mine != 0);
+        const unsigned several = __ballot_sync(0xffffffffu, (mine & (mine - 1)) != 0);
         unsigned e;
-        if ((at & (at - 1)) == 0) {  // nearly always: one lane has the largest high word
-            e = __shfl_sync(0xffffffffu, (unsigned)(lane + 32 * bi), __ffs(at) - 1);
+        if ((at & (at - 1)) == 0 && several == 0) {
+            e = __shfl_sync(0xffffffffu, (unsigned)lane + 32u * (unsigned)(__ffs(mine) - 1), __ffs(at) - 1);
         } else {
-            const unsigned ml = __reduce_max_sync(0xffffffffu, hi == mh ? lo : 0u);
-            e = __reduce_min_sync(0xffffffffu, hi == mh && lo == ml ? (unsigned)(lane + 32 * bi) : ~0u);
+            unsigned lo = 0, bi = 0;
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                if (((mine >> i) & 1u) && ((unsigned)key[i] > lo || !(mine & ((1u << i) - 1)))) {
+                    lo = (unsigned)key[i];
+                    bi = i;
+                }
+            const unsigned ml = __reduce_max_sync(0xffffffffu, mine ? lo : 0u);
+            e = __reduce_min_sync(0xffffffffu, mine && lo == ml ? (unsigned)lane + 32u * bi : ~0u);
         }
         const unsigned hit = (e & 31u) == (unsigned)lane ? 1u << (e >> 5) : 0u;  // (a bit, so that key stays in registers)
 #pragma unroll
