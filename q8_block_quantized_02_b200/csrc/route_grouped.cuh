@@ -4,6 +4,10 @@
 // fp32 scores would tie or swap where the definition does not.  They are
 // compared as 64-bit integers of the same order, which costs no double
 // operations.
+// Latency bounds it up to some hundred tokens (1 token of 60 experts 4.7 us, 16
+// of 256 6.1 us, launches included), then the integer instructions: about 2000
+// a token, 14.2 us for 4096 tokens of 256 experts in 8 groups (their bytes: 0.7
+// us).
 #pragma once
 
 #include "q8_device.cuh"

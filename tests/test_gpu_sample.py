@@ -136,7 +136,7 @@ def test_mass_in_few_tokens(top_p):
     check(l, top_p=top_p, temperature=2.5, min_p=0.01, u=g.random(8).astype(np.float32))
 
 
-@pytest.mark.parametrize("V", [1024, 1025, 19008, 19009, 32768, 32769])
+@pytest.mark.parametrize("V", [1024, 1025, 20064, 20065, 32768, 32769])
 @pytest.mark.parametrize("N", [1, 20, 75, 149, 161])
 def test_cluster_sizes(V, N):
     """Around the sizes and batches at which a row takes another number of CTAs."""
