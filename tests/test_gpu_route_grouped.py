@@ -97,3 +97,16 @@ def test_rows_past_the_batch_are_left_alone():
     idx, w = t.full((T + 3, k), -9, dtype=t.int32, device="cuda"), t.full((T + 3, k), 9.0, device="cuda")
     q8().q8_moe_route_grouped(l, None, T, E, k, 2, 1, 1, 0, 0, 1.0, idx, w)
     assert (idx[T:] == -9).all() and (w[T:] == 9.0).all() and (idx[:T] >= 0).all()
+
+
+def test_host_and_misaligned_pointers_are_refused():
+    t = torch()
+    m = q8()
+    l, b = t.zeros(1, 8, device="cuda"), t.zeros(8, device="cuda")
+    idx, w = t.zeros(1, 2, dtype=t.int32, device="cuda"), t.zeros(1, 2, device="cuda")
+    for args, status in (((l.cpu(), b, idx, w), 4), ((l, b.cpu(), idx, w), 4), ((l, b, idx.cpu(), w), 4), ((l, b, idx, w.cpu()), 4),
+                         ((l.data_ptr() + 2, b, idx, w), 3), ((l, b.data_ptr() + 1, idx, w), 3), ((l, b, idx.data_ptr() + 2, w), 3),
+                         ((l, b, idx, w.data_ptr() + 2), 3)):
+        with pytest.raises(m.Q8Error) as e:
+            m.q8_moe_route_grouped(args[0], args[1], 1, 8, 2, 2, 1, 1, 0, 0, 1.0, args[2], args[3])
+        assert e.value.status == status

@@ -277,3 +277,17 @@ def test_captured_replays_and_another_stream():
         got = (token.clone(), prob.clone())
         q8().q8_sample(*args)
         assert t.equal(got[0], token) and t.equal(got[1], prob)
+
+
+def test_host_and_misaligned_pointers_are_refused():
+    t = torch()
+    m = q8()
+    N, V = 2, 100
+    l, u, p = t.zeros(N, V, device="cuda"), t.zeros(N, device="cuda"), t.zeros(N, device="cuda")
+    tok = t.zeros(N, dtype=t.int32, device="cuda")
+    good = [l, p, tok, p, p, u, tok, p]
+    for i in range(8):
+        for wrong, status in ((good[i].cpu(), 4), (good[i].data_ptr() + 2, 3)):
+            with pytest.raises(m.Q8Error) as e:
+                m.q8_sample(*(good[:i] + [wrong] + good[i + 1:]), N, V, V)
+            assert e.value.status == status, (i, e.value.status)
