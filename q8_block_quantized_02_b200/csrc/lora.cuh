@@ -2,24 +2,25 @@
 //   u = A_a x_n,  y_n = residual_n + scale_a B_a u,   a = adapter[n],
 // A_a [R][K], B_a [M][R] (rows past the adapter's rank are not read).
 //
-// One thread-block cluster per token; the cluster of the first of up to
-// kLoraTok tokens that share an adapter serves them all, so an adapter is read
-// once per kLoraTok of its tokens, and the clusters of the others leave.  The
-// cluster's CTAs split K for u, exchange the partial u over distributed shared
-// memory (added in rank order) and split M for B u.  Sums are fp32 in a fixed
-// order.
+// One thread-block cluster per token.  Its CTAs split K for u, exchange the
+// partial u over distributed shared memory (added in rank order) and split M for
+// B u.  Sums are fp32 in a fixed order.  The clusters of tokens that share an
+// adapter each read it, through L2: all clusters run at once, so serving several
+// tokens by one of them would leave the others' SMs idle (tried, up to four
+// tokens a cluster: 3584 x 18944, 16 rows of one bf16 adapter of rank 128, 34 us
+// against 17; 4 rows, rank 64, 13.4 against 8.0).
 //
-// What it reads is all it costs.  For u a warp takes up to 8 rows of A
-// at a time and loads the next columns into registers while it multiplies the
-// last: 64 KB in flight per SM.  (Rings of asynchronous copies in shared memory
-// in its place, twice as deep, measured slower: what shared memory takes, the
-// L1 cache lacks for loads in flight.)  B is fetched to L2 while u is
-// exchanged; loading its next rows while the last are multiplied gave the large
-// calls 3% and cost the small ones 4% in code.
-// One B200: alone on 3584 x 18944, 16 bf16 adapters of rank 52 to 128, 24 us
+// What it reads is all it costs.  For u a warp takes 16 bytes' worth of rows of A
+// (8 of two bytes, 4 of fp32) at a time and loads the next columns into registers
+// while it multiplies the last: 64 KB in flight per SM.  (Rings of asynchronous
+// copies in shared memory in its place, twice as deep, measured slower: what
+// shared memory takes, the L1 cache lacks for loads in flight.)  B is fetched to
+// L2 while u is exchanged; loading its next rows while the last are multiplied
+// gave the large calls 3% and cost the small ones 4% in code.
+// One B200: alone on 3584 x 18944, 16 bf16 adapters of rank 52 to 128, 23.6 us
 // for 67 MB (of which the rank-128 clusters read 57 GB/s per SM for u); alone
-// on 3584 x 3584, one fp32 adapter of rank 32 for 16 rows, 10.6 us, all
-// latency: indices, x and A, the exchange, B.
+// on 3584 x 3584, one fp32 adapter of rank 32 for 16 rows, 7.7 us, all latency:
+// indices, x and A, the exchange, B.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,7 +34,6 @@ namespace q8 {
 
 constexpr int kLoraThreads = 512;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kLoraTok = 4;        // tokens a cluster serves
 constexpr int kLoraMaxR = 128;
 constexpr int kLoraChunk = 3328;   // most columns of x staged at a time (a multiple of 256)
 constexpr int kLoraBlock = 64;     // rows of y a warp gathers before it writes them
@@ -72,10 +72,6 @@ struct Lora8<float> {
         a = lora_ldg(reinterpret_cast<const ulonglong2 *>(p));
         b = lora_ldg(reinterpret_cast<const ulonglong2 *>(p) + 1);
     }
-    __device__ __forceinline__ void from(const void *shared) {
-        a = reinterpret_cast<const ulonglong2 *>(shared)[0];
-        b = reinterpret_cast<const ulonglong2 *>(shared)[1];
-    }
     __device__ __forceinline__ void zero() { a = b = make_ulonglong2(0, 0); }
     __device__ __forceinline__ static uint64_t first(uint64_t v, int n) {
         return n >= 2 ? v : n == 1 ? v & 0xffffffffull : 0;
@@ -99,7 +95,6 @@ struct Lora8Short {  // two-byte elements
         const ulonglong2 v = lora_ldg(static_cast<const ulonglong2 *>(p));
         q = *reinterpret_cast<const uint4 *>(&v);
     }
-    __device__ __forceinline__ void from(const void *shared) { q = *static_cast<const uint4 *>(shared); }
     __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ static uint32_t first(uint32_t v, int n) { return n >= 2 ? v : n == 1 ? v & 0xffffu : 0; }
     __device__ __forceinline__ void keep(int n) {
@@ -134,17 +129,14 @@ __device__ __forceinline__ float lora_sum2(uint64_t v) {
     return f.x + f.y;
 }
 
-// Dynamic shared memory: x of a cluster's tokens (at most `tokens`).
-inline size_t lora_smem_bytes(int chunk, int tokens) {
-    return (size_t)(tokens >= 3 ? kLoraTok : tokens) * chunk * 4;
-}
+// Dynamic shared memory: a chunk of x.
+inline size_t lora_smem_bytes(int chunk) { return (size_t)chunk * 4; }
 
 struct LoraShared {
-    float part[kLoraMaxR * kLoraTok * 2];  // sums of a task: [rows of its group][tokens]
-    float pu[kLoraMaxR * kLoraTok];        // this CTA's share of u, read by the cluster
-    __align__(8) float us[kLoraTok][kLoraMaxR];  // scale u
-    float ys[kLoraWarps][kLoraTok][kLoraBlock];
-    int tok[kLoraTok];
+    float part[kLoraMaxR];             // sums of a task: [rows of its group]
+    float pu[kLoraMaxR];               // this CTA's share of u, read by the cluster
+    __align__(8) float us[kLoraMaxR];  // scale u
+    float ys[kLoraWarps][kLoraBlock];
 };
 
 // Halves the n values that a lane holds (the other half goes to the lane `off`
@@ -161,16 +153,33 @@ __device__ __forceinline__ void lora_fold(float (&v)[C], int lane, int off, int 
     }
 }
 
-// One cluster's work for nt <= NT tokens of one adapter.
-template <typename T, int NT>
-__device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, uint8_t *smem, uint32_t CL, uint32_t rank,
-                                             int ad, int nt, int r) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+template <typename T>
+__global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs a) {
+    extern __shared__ __align__(16) uint8_t lora_smem[];
+    __shared__ LoraShared sh;
     constexpr int ES = sizeof(T);
-    constexpr int RB = (NT == 1 ? 16 : 8) / ES;     // rows of A a warp takes together (what the registers hold)
-    constexpr int V = RB * NT;                      // values a task sums (a power of two, at most 32)
-    const int half = a.chunk / 8;
-    ulonglong2 *xs = reinterpret_cast<ulonglong2 *>(smem);  // [token][half of 8][chunk / 8]
+    constexpr int RB = 16 / ES;  // rows of A a warp takes together (what the registers hold)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t CL;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(CL));
+    const uint32_t rank = cluster_ctarank();
+    const int n = blockIdx.x / CL;
+    pdl_wait_and_trigger();
+
+    const float *x = a.x + n * a.K;
+    const float *res = a.res ? a.res + n * a.M : nullptr;
+    float *y = a.y + n * a.M;
+    // this CTA's rows of y
+    const int64_t m_per = (a.M + CL - 1) / CL;
+    const int64_t m0 = min(a.M, m_per * rank), m1 = min(a.M, m0 + m_per);
+    const int ad = __ldg(a.adapter + n);
+    if (ad < 0 || ad >= a.n_adapters) {
+        if (ad >= a.n_adapters && rank == 0 && tid == 0) record_error(kErrBadAdapter);
+        for (int64_t m = m0 + tid; m < m1; m += kLoraThreads) y[m] = res ? res[m] : 0.f;
+        return;  // the whole cluster
+    }
+    int r = a.R;
+    if (a.rank) r = min(max(__ldg(a.rank + ad), 0), a.R);
 
     // u: this CTA's columns [k0, k1)
     const int64_t k_per = ((a.K / 32 + CL - 1) / CL) * 32;
@@ -179,7 +188,9 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
     const int groups = (r + RB - 1) / RB;
     const int ks = groups > 0 ? max(1, kLoraWarps / groups) : 1;  // warps that share a row group
     const int tasks = groups * ks;
-    for (int i = tid; i < tasks * V; i += kLoraThreads) sh.part[i] = 0.f;
+    const int half = a.chunk / 8;
+    ulonglong2 *xs = reinterpret_cast<ulonglong2 *>(lora_smem);  // [half of 8][chunk / 8]
+    for (int i = tid; i < tasks * RB; i += kLoraThreads) sh.part[i] = 0.f;
     for (int64_t c0 = k0; c0 < k1; c0 += a.chunk) {
         const int units = (int)min((int64_t)a.chunk, k1 - c0) / 8;
         // unit `un` of 8 columns of a task's rows; past the last unit and the last
@@ -203,38 +214,25 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
             load(even, (warp % ks) * 32 + lane);
         }
         __syncthreads();  // (x of the last chunk is no longer read)
-        for (int i = tid; i < NT * units * 2; i += kLoraThreads) {
-            const int t = i / (units * 2), q = i % (units * 2);
-            xs[(t * 2 + (q & 1)) * half + (q >> 1)] =
-                t < nt ? __ldg(reinterpret_cast<const ulonglong2 *>(a.x + sh.tok[t] * a.K + c0) + q)
-                       : make_ulonglong2(0, 0);
-        }
+        for (int q = tid; q < units * 2; q += kLoraThreads)
+            xs[(q & 1) * half + (q >> 1)] = __ldg(reinterpret_cast<const ulonglong2 *>(x + c0) + q);
         __syncthreads();
 #pragma unroll 1
         for (int task = warp; task < tasks; task += kLoraWarps) {
-            uint64_t acc2[V];  // even and odd columns
+            uint64_t acc2[RB];  // even and odd columns
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc2[i] = 0;
+            for (int j = 0; j < RB; ++j) acc2[j] = 0;
             auto multiply = [&](const Lora8<T>(&a8)[RB], int un) {
                 if (un >= units) return;
-                ulonglong2 x[NT][2];
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    x[t][0] = xs[(t * 2) * half + un];
-                    x[t][1] = xs[(t * 2 + 1) * half + un];
-                }
+                const ulonglong2 x0 = xs[un], x1 = xs[half + un];
 #pragma unroll
                 for (int j = 0; j < RB; ++j) {
                     uint64_t w[4];
                     a8[j].get(w);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        uint64_t &v = acc2[j * NT + t];
-                        v = fma_f32x2(w[0], x[t][0].x, v);
-                        v = fma_f32x2(w[1], x[t][0].y, v);
-                        v = fma_f32x2(w[2], x[t][1].x, v);
-                        v = fma_f32x2(w[3], x[t][1].y, v);
-                    }
+                    acc2[j] = fma_f32x2(w[0], x0.x, acc2[j]);
+                    acc2[j] = fma_f32x2(w[1], x0.y, acc2[j]);
+                    acc2[j] = fma_f32x2(w[2], x1.x, acc2[j]);
+                    acc2[j] = fma_f32x2(w[3], x1.y, acc2[j]);
                 }
             };
             const int step = ks * 32;
@@ -250,28 +248,26 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
                 if (un - lane + 2 * step < units) load(even, un + 2 * step);
                 multiply(odd, un + step);
             }
-            float acc[V];
+            float acc[RB];
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = lora_sum2(acc2[i]);
-            int off = 16, n = V;
+            for (int j = 0; j < RB; ++j) acc[j] = lora_sum2(acc2[j]);
+            int off = 16, left = RB;
 #pragma unroll
             for (int st = 0; st < 5; ++st, off >>= 1) {
-                if (n > 1) {
-                    lora_fold<V>(acc, lane, off, n);
-                    n >>= 1;
+                if (left > 1) {
+                    lora_fold<RB>(acc, lane, off, left);
+                    left >>= 1;
                 } else {
                     acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], off);
                 }
             }
-            // a lane holds the value whose index is its top bits
-            if (lane % (32 / V) == 0) sh.part[task * V + lane / (32 / V)] += acc[0];
+            // a lane holds the row whose index is its top bits
+            if (lane % (32 / RB) == 0) sh.part[task * RB + lane / (32 / RB)] += acc[0];
         }
     }
 
-    // B: the CTA's rows [m0, m1), a contiguous part of them for each warp, sent
-    // for (to L2) while u is exchanged
-    const int64_t m_per = (a.M + CL - 1) / CL;
-    const int64_t m0 = min(a.M, m_per * rank), m1 = min(a.M, m0 + m_per);
+    // B: a contiguous part of the CTA's rows for each warp, sent for (to L2) while
+    // u is exchanged
     const int64_t w_per = (m1 - m0 + kLoraWarps - 1) / kLoraWarps;
     const int64_t w0 = min(m1, m0 + w_per * warp), w1 = min(m1, w0 + w_per);
     const T *B = static_cast<const T *>(a.B) + (int64_t)ad * a.M * a.R;
@@ -281,29 +277,26 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
 #pragma unroll 1
     for (int64_t m = w0 + lane * row_step; m < w1; m += 32 * row_step)
         for (int i = 0; i < lines; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(B + m * a.R + i * (128 / ES)));
-    if (a.res)
-        for (int t = 0; t < nt; ++t)
+    if (res)
 #pragma unroll 1
-            for (int64_t m = w0 + lane * 8; m < w1; m += 256)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(a.res + sh.tok[t] * a.M + m));
+        for (int64_t m = w0 + lane * 8; m < w1; m += 256) asm volatile("prefetch.global.L2 [%0];" ::"l"(res + m));
 
     __syncthreads();
-    for (int i = tid; i < r * NT; i += kLoraThreads) {
-        const int j = i / NT, t = i % NT;
+    if (tid < r) {
         float v = 0.f;
-        for (int s = 0; s < ks; ++s) v += sh.part[((j / RB) * ks + s) * V + (j % RB) * NT + t];
-        sh.pu[i] = v;
+        for (int s = 0; s < ks; ++s) v += sh.part[((tid / RB) * ks + s) * RB + tid % RB];
+        sh.pu[tid] = v;
     }
     const float sc = a.scale ? __ldg(a.scale + ad) : 1.f;
     cluster_sync_all();
-    for (int i = tid; i < kLoraMaxR * NT; i += kLoraThreads) {
+    if (tid < kLoraMaxR) {
         float v[16];
 #pragma unroll
         for (uint32_t p = 0; p < 16; ++p)
-            v[p] = p < CL && i < r * NT ? ld_cluster_f32(map_to_rank(smem_u32(&sh.pu[i]), p)) : 0.f;
+            v[p] = p < CL && tid < r ? ld_cluster_f32(map_to_rank(smem_u32(&sh.pu[tid]), p)) : 0.f;
 #pragma unroll
         for (uint32_t p = 1; p < 16; ++p) v[0] += v[p];
-        sh.us[i % NT][i / NT] = sc * v[0];
+        sh.us[tid] = sc * v[0];
     }
     // pu is not read any more; the barrier is waited for before the CTA ends
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -314,25 +307,20 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
     while (lanes < bu) lanes <<= 1;
     const int jc = lane & (lanes - 1), grp = lane / lanes, G = 32 / lanes;
     const int kept = min(max(r - jc * 8, 0), 8);  // what lies past the rank is not used
-    uint64_t uf[NT][4];
+    uint64_t uf[4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) uf[t][i] = *reinterpret_cast<const uint64_t *>(&sh.us[t][jc * 8 + 2 * i]);
+    for (int i = 0; i < 4; ++i) uf[i] = *reinterpret_cast<const uint64_t *>(&sh.us[jc * 8 + 2 * i]);
 #pragma unroll 1
     for (int64_t m = w0; m < w1; m += kLoraBlock) {
         const int rows = (int)min((int64_t)kLoraBlock, w1 - m);
-        float out[2][NT];  // the residuals, all loaded before any is stored over
+        float out[2];  // the residuals, loaded before any is stored over
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                out[h][t] = a.res && t < nt && lane + 32 * h < rows ? a.res[sh.tok[t] * a.M + m + lane + 32 * h] : 0.f;
+        for (int h = 0; h < 2; ++h) out[h] = res && lane + 32 * h < rows ? res[m + lane + 32 * h] : 0.f;
         // (kept short: code that runs once is paid for in instruction fetches)
-        constexpr int RT = NT == 4 ? 2 : 4;  // rows a lane takes together
+        constexpr int RT = 4;  // rows a lane takes together
 #pragma unroll 1
         for (int j = grp; j - grp < rows; j += RT * G) {
-            float v[RT][NT];
+            float v[RT];
             Lora8<T> q[RT];
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
@@ -344,80 +332,28 @@ __device__ __forceinline__ void lora_cluster(const LoraArgs &a, LoraShared &sh, 
                 if (kept < 8) q[i].keep(kept);
                 uint64_t w[4];
                 q[i].get(w);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    uint64_t s2 = mul_f32x2(w[0], uf[t][0]);
-                    s2 = fma_f32x2(w[1], uf[t][1], s2);
-                    s2 = fma_f32x2(w[2], uf[t][2], s2);
-                    s2 = fma_f32x2(w[3], uf[t][3], s2);
-                    v[i][t] = lora_sum2(s2);
-                }
+                uint64_t s2 = mul_f32x2(w[0], uf[0]);
+                s2 = fma_f32x2(w[1], uf[1], s2);
+                s2 = fma_f32x2(w[2], uf[2], s2);
+                s2 = fma_f32x2(w[3], uf[3], s2);
+                v[i] = lora_sum2(s2);
             }
 #pragma unroll 1
             for (int off = lanes >> 1; off > 0; off >>= 1)
 #pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) v[i][t] += __shfl_xor_sync(0xffffffffu, v[i][t], off);
+                for (int i = 0; i < RT; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], off);
             if (jc == 0)
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
-                    if (j + i * G < rows)
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) sh.ys[warp][t][j + i * G] = v[i][t];
+                    if (j + i * G < rows) sh.ys[warp][j + i * G] = v[i];
         }
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (t < nt && lane + 32 * h < rows)
-                    a.y[sh.tok[t] * a.M + m + lane + 32 * h] = out[h][t] + sh.ys[warp][t][lane + 32 * h];
+            if (lane + 32 * h < rows) y[m + lane + 32 * h] = out[h] + sh.ys[warp][lane + 32 * h];
         __syncwarp();
     }
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs a) {
-    extern __shared__ __align__(16) uint8_t lora_smem[];
-    __shared__ LoraShared sh;
-    const int tid = threadIdx.x, lane = tid & 31;
-    uint32_t CL;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(CL));
-    const uint32_t rank = cluster_ctarank();
-    const int n = blockIdx.x / CL;
-    pdl_wait_and_trigger();
-
-    // which tokens this cluster serves
-    const int mine = lane < a.N ? __ldg(a.adapter + lane) : -1;
-    const int ad = __shfl_sync(0xffffffffu, mine, n);
-    if (ad < 0 || ad >= a.n_adapters) {
-        if (ad >= a.n_adapters && rank == 0 && tid == 0) record_error(kErrBadAdapter);
-        const int64_t m_per = (a.M + CL - 1) / CL;
-        const int64_t m0 = min(a.M, m_per * rank), m1 = min(a.M, m0 + m_per);
-        for (int64_t m = m0 + tid; m < m1; m += kLoraThreads)
-            a.y[n * a.M + m] = a.res ? a.res[n * a.M + m] : 0.f;
-        return;  // the whole cluster
-    }
-    unsigned same = __ballot_sync(0xffffffffu, lane < a.N && mine == ad);
-    if (__popc(same & ((1u << n) - 1)) % kLoraTok != 0) return;  // the whole cluster: another one serves it
-    same &= ~((1u << n) - 1);
-    const int nt = min(__popc(same), kLoraTok);
-#pragma unroll
-    for (int i = 0; i < kLoraTok; ++i) {
-        if (tid == 0) sh.tok[i] = same ? __ffs(same) - 1 : n;
-        same &= same - 1;
-    }
-    __syncthreads();
-    int r = a.R;
-    if (a.rank) r = min(max(__ldg(a.rank + ad), 0), a.R);
-    if (nt == 1)
-        lora_cluster<T, 1>(a, sh, lora_smem, CL, rank, ad, nt, r);
-    else if (nt == 2)
-        lora_cluster<T, 2>(a, sh, lora_smem, CL, rank, ad, nt, r);
-    else
-        lora_cluster<T, 4>(a, sh, lora_smem, CL, rank, ad, nt, r);
 }
 
 }  // namespace q8

@@ -928,7 +928,7 @@ static cudaError_t setup_lora_kernels(int max_smem) {
         cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)lora_smem_bytes(kLoraChunk, kLoraTok));
+                                 (int)lora_smem_bytes(kLoraChunk));
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -980,9 +980,9 @@ static q8_status run_lora(LoraArgs a, int dtype, cudaStream_t stream, bool early
     Q8_CHECK(device_info(&dev));
     const LoraKernel kern = lora_kernel_for(dtype);
     const int cl = cluster_for(dtype, a.N, reinterpret_cast<const void *>(kern), kLoraThreads,
-                               lora_smem_bytes(kLoraChunk, kLoraTok), dev->sms, 16, kLoraMinCluster);
+                               lora_smem_bytes(kLoraChunk), dev->sms, 16, kLoraMinCluster);
     a.chunk = (int)std::min<int64_t>(kLoraChunk, round_up(ceil_div(a.K / 32, cl) * 32, 256));
-    return launch_cluster(early, kern, dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), lora_smem_bytes(a.chunk, a.N),
+    return launch_cluster(early, kern, dim3((unsigned)(a.N * cl)), dim3(kLoraThreads), lora_smem_bytes(a.chunk),
                           stream, "q8_lora launch", (unsigned)cl, a);
 }
 
@@ -990,10 +990,10 @@ static q8_status run_lora(LoraArgs a, int dtype, cudaStream_t stream, bool early
 // adds its product to y in place.  Beside a large projection the adapters'
 // kernel does not become resident early: its clusters would take SMs as the
 // kernel before leaves them, spread over the GPU, and the projection's clusters
-// then find room later (3584x18944, N = 16, rank 128: 87.7 us early, 80.4 not;
-// N = 4, rank 64: 59.0 and 58.1).  Beside a small one its launch latency counts
-// for more (896x4864, N = 1: 9.1 us early, 9.8 not; 3584x3584, N = 12: 54.5
-// and 54.8).
+// then find room later (3584x18944, N = 16, rank 128: 86.0 us early, 79.1 not;
+// N = 4, rank 64: 57.4 and 56.4).  Beside a small one its launch latency counts
+// for more (896x4864, N = 1: 7.9 us early, 8.3 not; 3584x3584, N = 12: 52.1 and
+// 51.8).
 constexpr int64_t kLoraEarlyMax = 16384;  // M + K below which it is launched early
 static q8_status run_gemv_lora(const void *W, const LoraArgs &a, int64_t N, int64_t n_adapters, int64_t R, int dtype,
                                cudaStream_t stream, bool split) {
