@@ -762,11 +762,11 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
                     const unsigned at1 = __ballot_sync(0xffffffffu, c1 >= (uint32_t)top_k);
                     b = g * kSampleGroup + (at0 ? __ffs(at0) - 1 : 31 + __ffs(at1));
                 }
-                if (lane == 0) sh.bin = b;
+                if (lane == 0) sh.count = (uint32_t)b;  // (with g < 0 other warps may still have to read g from sh.bin)
             }
             __syncthreads();
             // the elements down to that bin: gathered here, then sent to rank 0
-            const int b = sh.bin;
+            const int b = (int)sh.count;
             const float live = key_logit((uint32_t)(kt >> 32));
 #pragma unroll 2
             for (int j = tid; 4 * j < n; j += kSampleThreads) {

@@ -1,0 +1,27 @@
+"""GPU parity of q8_sample on rows and parameters whose threads settle a row together in few steps, against double
+precision (tests/test_sample_threads_cpu.py runs the same ones under schedules of its own)."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from test_gpu_sample import check
+
+pytestmark = pytest.mark.gpu
+
+NEG = -np.inf
+
+
+@pytest.mark.parametrize("N", [1, 16, 160])
+@pytest.mark.parametrize("live", [1, 20, 49])
+def test_fewer_live_tokens_than_top_k(N, live):
+    g = np.random.default_rng(N + live)
+    V = 32000
+    l = np.full((N, V), NEG, np.float32)
+    for n in range(N):
+        l[n, g.choice(V, live, replace=False)] = g.standard_normal(live).astype(np.float32) * 2
+    u = g.random(N).astype(np.float32)
+    check(l, top_k=50, u=u)
+    check(l, top_k=50, top_p=0.7, min_p=0.02, u=u)
+    cold = (g.standard_normal((N, V)) * 2).astype(np.float32)
+    check(cold, top_k=50, temperature=0.004, u=u)

@@ -1,0 +1,44 @@
+"""The sampler's threads, without a GPU: csrc/sample.cuh run by tests/cta_emulator.h under schedules that let one warp
+or CTA run as far ahead of the others as the barriers allow.  Whatever the schedule, the tokens are the
+double-precision reference's."""
+from __future__ import annotations
+
+import shutil
+
+import numpy as np
+import pytest
+
+import request_refs as refs
+import sample_emulator as emu
+
+NEG = -np.inf
+ORDERS = sorted(emu.orders(1))
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    if shutil.which("g++") is None:
+        pytest.skip("g++ not available")
+    return emu.build(str(tmp_path_factory.mktemp("sample")))
+
+
+def check(lib, l, order, cl=1, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, u=0.5, fill=0xa5):
+    l = np.atleast_2d(np.asarray(l, np.float32))
+    token, prob = emu.sample(lib, l, temperature, top_k, top_p, min_p, u, cl=cl, order=emu.orders(cl)[order], fill=fill)
+    at = lambda v, n: np.float32(np.broadcast_to(np.asarray(v, np.float64), (l.shape[0],))[n])
+    for n in range(l.shape[0]):
+        k = int(np.broadcast_to(np.asarray(top_k), (l.shape[0],))[n])
+        rt, rp, _ = refs.sample_row(l[n], at(temperature, n), k, at(top_p, n), at(min_p, n), at(u, n))
+        assert token[n] == rt, (n, token[n], rt)
+        # one rounding to fp32, and the fixed-point total's V roundings of 2^-44 of the largest weight
+        assert abs(prob[n] - rp) <= (2.0 ** -24 * 1.0001 + l.shape[1] * 2.0 ** -44) * rp + 2.0 ** -149, (n, prob[n], rp)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+def test_fewer_live_tokens_than_top_k(lib, order):
+    """A row masked down to a few tokens, and a cold one: fewer of the threads' maxima count than top_k asks for."""
+    g = np.random.default_rng(1)
+    l = (g.standard_normal((2, 2000)) * 2).astype(np.float32)
+    l[0, 20:] = NEG
+    check(lib, l, order, top_k=50, u=[0.3, 0.8], temperature=[1.0, 0.004])
+    check(lib, l[0], order, top_k=50, top_p=0.6, min_p=0.01, u=0.9)
