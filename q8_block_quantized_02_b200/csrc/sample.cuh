@@ -583,14 +583,15 @@ __device__ bool sample_filter(const SampleRow &s, u64 lo, u64 hi, u64 target, do
 }
 
 // Descending bitonic sort of one value a thread over the first `width` threads
-// (a power of two, 32 .. kSampleThreads).  Whole CTA.
-__device__ __forceinline__ u64 sample_sort(const SampleRow &s, u64 v, int width) {
+// (a power of two, 32 .. kSampleThreads).  `flip`: the half of the exchange
+// buffer that the next exchange writes, 0 at first and carried from one sort to
+// the next: a warp may still be reading the other half.  Whole CTA.
+__device__ __forceinline__ u64 sample_sort(const SampleRow &s, u64 v, int width, int &flip) {
     u64 *x = s.sh->mass;
-    int flip = 0;
     for (int k = 2; k <= width; k <<= 1)
         for (int j = k >> 1; j > 0; j >>= 1) {
             u64 o;
-            if (j >= 32) {  // two buffers in turn, so one barrier a step
+            if (j >= 32) {  // two halves in turn, so one barrier a step
                 x[flip + s.tid] = v;
                 __syncthreads();
                 o = x[flip + (s.tid ^ j)];
@@ -791,10 +792,10 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
             for (uint32_t p = 0; p < CL; ++p) all += s.inbox[p].sent;
             if (all <= kSampleThreads) {  // rank 0 settles the row
                 if (rank != 0) return;
-                int width = 32;
+                int width = 32, flip = 0;
                 while (width < (int)all) width *= 2;
                 // in the filters' order: top-k, top-p, min-p
-                const u64 e = sample_sort(s, tid < (int)all ? sh.list[tid] : 0, width);
+                const u64 e = sample_sort(s, tid < (int)all ? sh.list[tid] : 0, width, flip);
                 const float l = key_logit((uint32_t)(e >> 32));
                 bool keep = tid < min((int)all, top_k);
                 u64 w = keep ? s.weight(l) : 0, z;
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
                 keep = keep && e >= kmin;
                 // in index order: index and weight in one word (19 and 44 bits)
                 const uint32_t index = 0xffffffffu - (uint32_t)e;
-                const u64 y = sample_sort(s, keep ? ~((u64)index << 44 | w) : 0, width);
+                const u64 y = sample_sort(s, keep ? ~((u64)index << 44 | w) : 0, width, flip);
                 w = tid < width && y ? ~y & 0xfffffffffffull : 0;
                 const u64 inc = sample_scan(s, w, &z);
                 u64 r = (u64)((double)u * (double)z);

@@ -25,3 +25,12 @@ def test_fewer_live_tokens_than_top_k(N, live):
     check(l, top_k=50, top_p=0.7, min_p=0.02, u=u)
     cold = (g.standard_normal((N, V)) * 2).astype(np.float32)
     check(cold, top_k=50, temperature=0.004, u=u)
+
+
+@pytest.mark.parametrize("N", [1, 16, 160])
+@pytest.mark.parametrize("top_k", [20, 40, 50, 100, 128])
+def test_two_sorts_in_turn(N, top_k):
+    g = np.random.default_rng(N + top_k)
+    l = (g.standard_normal((N, 32000)) * 2).astype(np.float32)
+    for kw in ({}, dict(min_p=0.05), dict(top_p=0.8)):
+        check(l, top_k=top_k, u=g.random(N).astype(np.float32), **kw)

@@ -42,3 +42,14 @@ def test_fewer_live_tokens_than_top_k(lib, order):
     l[0, 20:] = NEG
     check(lib, l, order, top_k=50, u=[0.3, 0.8], temperature=[1.0, 0.004])
     check(lib, l[0], order, top_k=50, top_p=0.6, min_p=0.01, u=0.9)
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("top_k", [20, 40, 50, 100, 128])
+def test_two_sorts_in_turn(lib, order, top_k):
+    """Top-k without top-p sorts twice with nothing between; the exchange buffer's halves follow on."""
+    g = np.random.default_rng(2)
+    l = (g.standard_normal((3, 3000)) * 2).astype(np.float32)
+    check(lib, l, order, top_k=top_k, u=[0.1, 0.5, 0.9])
+    check(lib, l, order, top_k=top_k, min_p=0.05, u=[0.2, 0.6, 0.95])
+    check(lib, l, order, top_k=top_k, top_p=0.8, u=[0.2, 0.6, 0.95])
