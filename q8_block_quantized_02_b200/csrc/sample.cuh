@@ -633,7 +633,10 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const int tid = s.tid = threadIdx.x, warp = s.warp = tid >> 5, lane = s.lane = tid & 31;
     const uint32_t CL = s.CL, rank = s.rank;
     const int row = blockIdx.x / CL;
+    // what no input decides; the __syncthreads behind the load publishes it
     if (tid == 0) sh.short_n = sh.sent = 0;
+    if (tid < 128) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 128.0);  // 2^43 ...
+    for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.cnt[i] = 0;
     pdl_wait_and_trigger();
 
     // this CTA's logits: NaN counts as -inf, -0 as +0; the largest, lowest index first
@@ -691,8 +694,6 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
     float u = __ldg(a.u + row);
     u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
-    if (tid < 128) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 128.0);  // 2^43 ...
-    for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.cnt[i] = 0;
     s.weight.c = 184.66496523378733 / t64;  // 128 log2(e)
     s.weight.tab = sh.tab;
     const double min_log = min_p > 0.f ? t64 * log((double)fminf(min_p, 1.f)) : 0.0;

@@ -34,3 +34,11 @@ def test_two_sorts_in_turn(N, top_k):
     l = (g.standard_normal((N, 32000)) * 2).astype(np.float32)
     for kw in ({}, dict(min_p=0.05), dict(top_p=0.8)):
         check(l, top_k=top_k, u=g.random(N).astype(np.float32), **kw)
+
+
+@pytest.mark.parametrize("N,V", [(1, 3001), (16, 32000), (160, 32000), (4, 151936)])
+def test_rows_without_top_k_and_top_p(N, V):
+    g = np.random.default_rng(N + V)
+    l = (g.standard_normal((N, V)) * 2).astype(np.float32)
+    for kw in ({}, dict(min_p=0.05, temperature=0.7), dict(temperature=1.7)):
+        check(l, u=g.random(N).astype(np.float32), **kw)

@@ -53,3 +53,15 @@ def test_two_sorts_in_turn(lib, order, top_k):
     check(lib, l, order, top_k=top_k, u=[0.1, 0.5, 0.9])
     check(lib, l, order, top_k=top_k, min_p=0.05, u=[0.2, 0.6, 0.95])
     check(lib, l, order, top_k=top_k, top_p=0.8, u=[0.2, 0.6, 0.95])
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("fill", [0, 0xa5, 0xff])
+def test_weight_table_is_ready(lib, order, fill):
+    """Rows without top-k and top-p use the weight table right after the first cluster barrier's wait."""
+    g = np.random.default_rng(3)
+    l = (g.standard_normal((3, 3000)) * 2).astype(np.float32)
+    check(lib, l, order, u=[0.1, 0.5, 0.9], fill=fill)
+    check(lib, l, order, min_p=0.05, temperature=0.7, u=[0.2, 0.6, 0.95], fill=fill)
+    l[:, ::31] = np.inf
+    check(lib, l, order, u=[0.1, 0.5, 0.9], fill=fill)
