@@ -633,6 +633,9 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const int tid = s.tid = threadIdx.x, warp = s.warp = tid >> 5, lane = s.lane = tid & 31;
     const uint32_t CL = s.CL, rank = s.rank;
     const int row = blockIdx.x / CL;
+    // (the other CTAs' shared memory is theirs only once all of the cluster's have
+    // started: arrived at here, waited for behind the load)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     // what no input decides; the __syncthreads behind the load publishes it
     if (tid == 0) sh.short_n = sh.sent = 0;
     if (tid < 128) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 128.0);  // 2^43 ...
@@ -678,6 +681,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const u64 own = best;  // this thread's largest
     best = warp_max(best);
     if (lane == 0) sh.wsum[warp] = best;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA has started
     __syncthreads();
     if (warp == 0) {
         best = warp_max(lane < kSampleWarps ? sh.wsum[lane] : 0);

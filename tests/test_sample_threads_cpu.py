@@ -65,3 +65,14 @@ def test_weight_table_is_ready(lib, order, fill):
     check(lib, l, order, min_p=0.05, temperature=0.7, u=[0.2, 0.6, 0.95], fill=fill)
     l[:, ::31] = np.inf
     check(lib, l, order, u=[0.1, 0.5, 0.9], fill=fill)
+
+
+@pytest.mark.parametrize("order", sorted(emu.orders(2)))
+@pytest.mark.parametrize("cl,V", [(2, 3001), (3, 4100), (2, 6)])
+def test_no_access_to_a_cta_that_may_not_have_started(lib, order, cl, V):
+    """Shared memory of another CTA is touched only behind a cluster barrier, and never once that CTA has ended."""
+    g = np.random.default_rng(4)
+    l = (g.standard_normal((2, V)) * 2).astype(np.float32)
+    for kw in ({}, dict(temperature=0.0), dict(top_k=40), dict(top_p=0.9)):
+        check(lib, l, order, cl=cl, u=[0.2, 0.85], **kw)
+    check(lib, np.full((1, V), NEG), order, cl=cl)
