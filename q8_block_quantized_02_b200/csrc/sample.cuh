@@ -159,6 +159,13 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
     return v;
 }
 
+// Where the uniform number lies in a mass of z: below 1 at the floor of u z, from
+// 1 on at the last unit, which is the last kept token's however small it is.
+__device__ __forceinline__ u64 sample_place(float u, u64 z) {
+    const u64 r = u < 1.f ? (u64)((double)u * (double)z) : z - 1;
+    return min(r, z - 1);
+}
+
 // Fixed-point weight of a logit (mx: the row's largest, finite).
 // 2^(43 - (k + r) / 128) with k = round(128 log2(e) (mx - l) / T): a table of
 // 2^(43 - j / 128) and the Taylor polynomial of 2^(-r / 128) to the fourth
@@ -697,7 +704,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const float top_p = a.top_p ? __ldg(a.top_p + row) : 1.f;
     const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
     float u = __ldg(a.u + row);
-    u = u > 0.f ? fminf(u, 0.99999994f) : 0.f;
+    u = u > 0.f ? u : 0.f;
     s.weight.c = 184.66496523378733 / t64;  // 128 log2(e)
     s.weight.tab = sh.tab;
     const double min_log = min_p > 0.f ? t64 * log((double)fminf(min_p, 1.f)) : 0.0;
@@ -815,8 +822,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
                 const u64 y = sample_sort(s, keep ? ~((u64)index << 44 | w) : 0, width, flip);
                 w = tid < width && y ? ~y & 0xfffffffffffull : 0;
                 const u64 inc = sample_scan(s, w, &z);
-                u64 r = (u64)((double)u * (double)z);
-                if (r > z - 1) r = z - 1;
+                const u64 r = sample_place(u, z);
                 if (inc - w <= r && r < inc) sh.base = (uint32_t)(~y >> 44);
                 __syncthreads();
                 if (keep && index == sh.base) write(index, l, z);
@@ -1019,8 +1025,7 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     // the CTA that the uniform number falls into goes on alone
     u64 z = 0;
     for (uint32_t p = 0; p < CL; ++p) z += sh.tot[p];
-    u64 r = (u64)((double)u * (double)z);
-    if (r > z - 1) r = z - 1;
+    u64 r = sample_place(u, z);
     uint32_t owner = 0;
     while (owner < CL - 1 && r >= sh.tot[owner]) r -= sh.tot[owner++];
     if (owner != rank) return;

@@ -5,7 +5,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
-from test_gpu_sample import check
+from test_gpu_sample import check, sample
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,18 @@ def test_rows_without_top_k_and_top_p(N, V):
     l = (g.standard_normal((N, V)) * 2).astype(np.float32)
     for kw in ({}, dict(min_p=0.05, temperature=0.7), dict(temperature=1.7)):
         check(l, u=g.random(N).astype(np.float32), **kw)
+
+
+@pytest.mark.parametrize("V", [6, 5000, 151936])
+@pytest.mark.parametrize("kw", [{}, dict(top_k=3), dict(top_k=300), dict(min_p=1e-10), dict(top_p=0.5), dict(temperature=0.0)])
+def test_one_and_above_take_the_last_kept_token(V, kw):
+    """u >= 1 is the last kept token in index order, however small its share (e^-24 of the heavy one's here)."""
+    l = np.full((4, V), -4.0, np.float32)
+    l[:, 1], l[:, 4], l[:, V - 2] = 20.0, 0.5, 0.25
+    order = np.lexsort((np.arange(V), -l[0]))
+    k = kw.get("top_k", V)
+    last = 1 if "top_p" in kw or "temperature" in kw else int(order[:k].max()) if k < V else V - 1
+    if "min_p" in kw:  # w >= 1e-10 is l > -3.03
+        last = V - 2
+    token, _ = sample(l, u=[1.0, 1.5, np.inf, 3e38], **kw)
+    assert token.tolist() == [last] * 4

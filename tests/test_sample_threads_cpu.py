@@ -76,3 +76,15 @@ def test_no_access_to_a_cta_that_may_not_have_started(lib, order, cl, V):
     for kw in ({}, dict(temperature=0.0), dict(top_k=40), dict(top_p=0.9)):
         check(lib, l, order, cl=cl, u=[0.2, 0.85], **kw)
     check(lib, np.full((1, V), NEG), order, cl=cl)
+
+
+@pytest.mark.parametrize("kw,last", [({}, 5), (dict(top_k=3), 4), (dict(top_k=5), 4), (dict(min_p=1e-10), 5),
+                                     (dict(top_k=5, top_p=0.99999994), 1), (dict(top_p=0.5), 1), (dict(temperature=0.0), 1)])
+def test_one_and_above_take_the_last_kept_token(lib, kw, last):
+    """u >= 1 is the last kept token in index order, however small its share (e^-20 of the row here)."""
+    l = np.array([[0.0, 20.0, 0.0, 0.0, 0.5, 0.0]], np.float32)
+    for u in (1.0, 1.5, np.inf):
+        token, prob = emu.sample(lib, l, u=u, **kw)
+        assert token[0] == last, (u, token)
+    token, _ = emu.sample(lib, l, u=np.nextafter(np.float32(1), np.float32(0)), **kw)
+    assert token[0] == 1  # the largest number below 1 still falls into the heavy token
