@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kLoraThreads, 1) lora_kernel(const LoraArgs a)
             v[p] = p < CL && tid < r ? ld_cluster_f32(map_to_rank(smem_u32(&sh.pu[tid]), p)) : 0.f;
 #pragma unroll
         for (uint32_t p = 1; p < 16; ++p) v[0] += v[p];
-        sh.us[tid] = sc * v[0];
+        sh.us[tid] = tid < r ? sc * v[0] : 0.f;  // (an infinite scale times nothing is not NaN)
     }
     // pu is not read any more; the barrier is waited for before the CTA ends
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
