@@ -363,7 +363,7 @@ typedef enum q8_score { Q8_SCORE_SOFTMAX = 0, Q8_SCORE_SIGMOID = 1 } q8_score;
  * largest c, and the topk_group best groups stay (n_group = 1: all experts).
  * idx[t]: the top_k experts of those by c, descending; equal scores, of groups
  * and of experts, go to the lowest index.  w[t][j] = s[idx] (not c), divided
- * by the picks' sum when renormalize != 0, times scale.
+ * by the picks' sum when renormalize != 0, times scale (any finite number).
  * Scores are held and compared in double, w is rounded once.  NaN logits count
  * as -inf; a score of -inf logits is 0, and +inf logits share a softmax; an
  * exponential below e^-708 is 0; a NaN

@@ -6,6 +6,7 @@
 // the caller's stream with programmatic dependent launch; nothing here
 // allocates, frees or synchronises (q8_read_device_error excepted).
 #include <atomic>
+#include <cmath>
 
 #include "host_common.cuh"
 #include "pack.cuh"
@@ -1298,7 +1299,7 @@ q8_status q8_moe_route_grouped(const float *logits, const float *bias, int64_t T
     if (n_group > 1 && group_top > E / n_group) return Q8_ERR_SHAPE;
     if (score != Q8_SCORE_SOFTMAX && score != Q8_SCORE_SIGMOID) return Q8_ERR_INVALID;
     if (renormalize != 0 && renormalize != 1) return Q8_ERR_INVALID;
-    if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return Q8_ERR_INVALID;  // NaN or infinite
+    if (!std::isfinite(scale)) return Q8_ERR_INVALID;
     Q8_CHECK(check_aligned4(logits, false));
     Q8_CHECK(check_aligned4(bias, true));
     Q8_CHECK(check_aligned4(idx, false));
