@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -252,11 +254,32 @@ inline q8_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
 }
 
 // How many clusters of `cluster_x` CTAs of `kernel` (threads, dynamic shared
-// memory) the current device runs at once; cached per (device, kernel,
-// threads, smem, cluster size).  Clusters are placed within one GPC, so with
-// one CTA per SM a cluster size that does not divide a GPC's SMs leaves SMs
-// idle: 28 clusters of 5 do not fit at once on a 148-SM part (26 do), and the
-// last ones would run as a second wave.  0 when the query fails.
+// memory) the current device runs at once.  Clusters are placed within one GPC,
+// so with one CTA per SM a cluster size that does not divide a GPC's SMs leaves
+// SMs idle: 28 clusters of 5 do not fit at once on a 148-SM part (26 do), and
+// the last ones would run as a second wave.  -1 when the query fails.
+inline int query_active_clusters(const void *kernel, int threads, size_t smem, int cluster_x) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cluster_x);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster_x;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();  // not sticky; clear it
+        return -1;
+    }
+    return n;
+}
+
+// query_active_clusters cached per (device, kernel, threads, smem, cluster
+// size), for the planners that ask on every call.  0 when the query fails.
 inline int max_active_clusters(const void *kernel, int threads, size_t smem, int cluster_x) {
     struct Entry {
         int dev;
@@ -276,24 +299,33 @@ inline int max_active_clusters(const void *kernel, int threads, size_t smem, int
         if (cache[i].dev == dev && cache[i].k == kernel && cache[i].threads == threads && cache[i].smem == smem &&
             cache[i].cx == cluster_x)
             return cache[i].n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)cluster_x);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster_x;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();  // not sticky; clear it
-        return 0;
-    }
+    const int n = query_active_clusters(kernel, threads, smem, cluster_x);
+    if (n < 0) return 0;
     if (used < 64) cache[used++] = Entry{dev, kernel, threads, smem, cluster_x, n};
     return n;
+}
+
+// The largest cluster, of at most `most` CTAs, of which `n` run at once (one CTA
+// per SM), or `least`.  Found once per device, kernel (`slot`) and n <= 160, in a
+// table of its own: the sizes tried would crowd the planners' cache.  An answer
+// that rests on a failed query serves its call only.
+inline int cluster_for(int slot, int64_t n, const void *kernel, int threads, size_t smem, int sms, int most, int least) {
+    static std::atomic<signed char> known[kMaxDevices][4][161];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || n > 160) return least;
+    std::atomic<signed char> &k = known[dev][slot][n];
+    int cl = k.load(std::memory_order_relaxed);
+    if (cl == 0) {
+        bool sure = true;
+        for (cl = 16; cl > 1; --cl) {
+            if (n * cl > sms) continue;
+            const int fit = query_active_clusters(kernel, threads, smem, cl);
+            if (fit >= n) break;
+            sure = sure && fit >= 0;
+        }
+        if (sure) k.store((signed char)cl, std::memory_order_relaxed);
+    }
+    return std::max(least, std::min(cl, most));
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -958,22 +958,6 @@ static q8_status lora_check(const LoraArgs &a, int64_t N, int64_t n_adapters, in
     return check_aligned4(a.res, true);
 }
 
-// The largest cluster, of at most `most` CTAs, of which `n` run at once (one CTA
-// per SM), or `least`.  Found once per device, kernel (`slot`) and n; n <= 160.
-static int cluster_for(int slot, int64_t n, const void *kernel, int threads, size_t smem, int sms, int most, int least) {
-    static std::atomic<signed char> known[kMaxDevices][4][161];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || n > 160) return least;
-    std::atomic<signed char> &k = known[dev][slot][n];
-    int cl = k.load(std::memory_order_relaxed);
-    if (cl == 0) {
-        for (cl = 16; cl > 1; --cl)
-            if (n * cl <= sms && max_active_clusters(kernel, threads, smem, cl) >= n) break;
-        k.store((signed char)cl, std::memory_order_relaxed);
-    }
-    return std::max(least, std::min(cl, most));
-}
-
 // A cluster per token, of the most CTAs with which the clusters of all tokens
 // run at once.
 static q8_status run_lora(LoraArgs a, int dtype, cudaStream_t stream, bool early) {
