@@ -130,9 +130,11 @@ def _ptr(t):
 
 def _stream(s):
     if s is None:
-        # the raw handle of the current stream: a Stream object costs 3 us more per call
+        # the raw handle of the current stream: a Stream object costs 3 us more per
+        # call (torch offers the handle only under a private name)
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
