@@ -645,7 +645,6 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     // what no input decides; the __syncthreads behind the load publishes it
     if (tid == 0) sh.short_n = sh.sent = 0;
-    if (tid < 128) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 128.0);  // 2^43 ...
     for (int i = tid; i < kSampleBins; i += kSampleThreads) sh.cnt[i] = 0;
     pdl_wait_and_trigger();
 
@@ -695,7 +694,9 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
         if (lane < (int)CL) st_cluster_u64(map_to_rank(smem_u32(&s.inbox[rank].best), lane), best);
     }
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    // the row's parameters, while the barrier completes
+    // the row's parameters and the weight table, while the barrier completes (at
+    // the kernel's start the table's exponentials delay the load of rows that wait
+    // for others to end: 128 rows, mixed, 93.0 us against 91.4)
     float temp = a.temperature ? __ldg(a.temperature + row) : 1.f;
     const bool greedy = !(temp > 0.f);
     temp = fminf(temp, 3.402823466e38f);
@@ -705,10 +706,12 @@ __global__ void __launch_bounds__(kSampleThreads, PER_SM) sample_kernel(const Sa
     const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
     float u = __ldg(a.u + row);
     u = u > 0.f ? u : 0.f;
+    if (tid < 128) sh.tab[tid] = 8796093022208.0 * exp2(-tid / 128.0);  // 2^43 ...
     s.weight.c = 184.66496523378733 / t64;  // 128 log2(e)
     s.weight.tab = sh.tab;
     const double min_log = min_p > 0.f ? t64 * log((double)fminf(min_p, 1.f)) : 0.0;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    __syncthreads();  // the table, which was written behind the arrive
     best = warp_max(lane < (int)CL ? s.inbox[lane].best : 0);
     float mx = key_logit((uint32_t)(best >> 32));
     if (mx == -INFINITY || greedy) {  // nothing to draw from, or greedy
