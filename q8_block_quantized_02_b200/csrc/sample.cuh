@@ -103,7 +103,8 @@ struct alignas(16) SampleShared {
     int bin;
 };
 
-// (the logits that follow the inboxes are stored four at a time)
+// the logits that follow the inboxes are stored four at a time
+static_assert(sizeof(SampleShared) % 16 == 0 && sizeof(SampleInbox) % 16 == 0, "the logits lie on a 16-byte boundary");
 __host__ __device__ inline size_t sample_smem_bytes(int slice, int cl) {
     return sizeof(SampleShared) + (size_t)cl * sizeof(SampleInbox) + (size_t)slice * 4;
 }
