@@ -221,7 +221,7 @@ static inline float q8_argmax_value(uint64_t key) {
  * Any logits are defined: NaN counts as -inf; a logit of -inf is never drawn;
  * +inf logits share the draw between them; a row with nothing above -inf gives
  * token -1, prob 0.  u is taken into [0, 1) (below 0 and NaN: 0; 1 and above:
- * the last kept token).  The sums are exact in units of 2^-43 of the largest
+ * the last kept token, however small its share).  The sums are exact in units of 2^-43 of the largest
  * weight, each weight rounded once (weights below 2^-44 are never drawn), so a
  * token does not depend on the order of any sum: the same from run to run.
  * One launch, no workspace.  1 <= N <= 65536, V <= 524288. */
@@ -249,8 +249,9 @@ typedef enum q8_dtype { Q8_F32 = 0, Q8_F16 = 1, Q8_BF16 = 2 } q8_dtype;
  *   y itself, any other overlap is undefined.  x: [N][K] fp32; y: [N][M] fp32.
  * fp32 sums in a fixed order: |y - exact| <= 2^-24 times (K/128 + 64) times
  *   |scale| sum_j |B_mj| sum_k |A_jk x_k|, plus the roundings of the stored
- *   value; bit-identical from run to run.  An adapter's matrices are read once
- *   for every 4 of its tokens.  One launch.
+ *   value; bit-identical from run to run.  Every token reads its adapter's
+ *   matrices; tokens that share an adapter find them in L2 where they fit.  One
+ *   launch.
  * K a multiple of 32, R a multiple of 8 up to 128, N <= 16, M <= 2^25. */
 q8_status q8_lora(const float *x, const void *A, const void *B, const int32_t *rank, const float *scale,
                   const int32_t *adapter, const float *residual, float *y, int64_t M, int64_t K, int64_t N,

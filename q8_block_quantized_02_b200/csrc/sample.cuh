@@ -26,12 +26,12 @@
 //     elements copied to every CTA; the sums show the cut in the window, or,
 //     where the estimate was off, that a histogram of exact masses has to find
 //     it.
-// So a row takes two to four cluster barriers and at most one pass over its
-// weights; only long runs of ties take more rounds.
+// So a row takes three to six cluster barriers, the first behind the load, and at
+// most one pass over its weights; only long runs of ties take more rounds.
 // What bounds it is latency (barriers, scans, instructions that are fetched to
 // run once) and, for top-p, the pass over the weights: 11 double operations
-// each.  One B200, V = 152064, 1 / 16 / 128 rows: no filter 8 / 13 / 69 us,
-// top-k 50 10 / 12 / 60, top-p 0.9 17 / 24 / 125; the logits' bytes at the
+// each.  One B200, V = 152064, 1 / 16 / 128 rows: no filter 8 / 13 / 70 us,
+// top-k 50 10 / 12 / 61, top-p 0.9 18 / 24 / 126; the logits' bytes at the
 // measured 6.5 TB/s are 0.1 / 1.5 / 12 us.
 #pragma once
 
@@ -48,8 +48,8 @@ constexpr int kSampleGroups = kSampleBins / kSampleGroup;
 constexpr int kSampleList = 1024;    // a count's or an exact mass's crossing bin
 constexpr int kSampleWindow = 2048;  // top-p's window
 // Largest top_k of the short path.  V = 152064, 1 / 16 / 128 rows: 14 / 16 / 70 us
-// at 256 there, 15 / 23 / 118 at 257 through the histogram of all elements
-// (10 / 12 / 60 at 50); its list holds 512.
+// at 256 there, 16 / 23 / 119 at 257 through the histogram of all elements
+// (10 / 12 / 61 at 50); its list holds 512.
 constexpr int kSampleShortK = 256;
 constexpr int kSampleMaxCluster = 16;
 constexpr int kSampleMaxSlice = 32768;  // logits per CTA
